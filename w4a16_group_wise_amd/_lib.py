@@ -1,4 +1,5 @@
-"""ctypes loader for libw4a16q.so and the exported C symbols (see include/w4a16q.h)."""
+"""ctypes loader for libw4a16q.so and the exported C symbols (see include/w4a16q.h and
+include/w4a16q_layer.h)."""
 from __future__ import annotations
 
 import ctypes
@@ -31,6 +32,13 @@ class AdamParams(ctypes.Structure):
     """w4q_adam_params of w4a16q.h"""
     _fields_ = [(n, ctypes.c_float) for n in ("lr_w", "lr_s", "beta1", "beta2", "eps", "weight_decay",
                                               "bias_c1", "bias_c2", "scale_min")]
+
+
+class MuonParams(ctypes.Structure):
+    """w4q_muon_params of w4a16q_layer.h"""
+    _fields_ = ([(n, ctypes.c_float) for n in ("lr", "momentum", "weight_decay", "update_scale")]
+                + [("coeffs", ctypes.c_float * 3), ("nesterov", ctypes.c_int), ("steps", ctypes.c_int),
+                   ("eps", ctypes.c_double)])
 
 
 SIGNATURES = {
@@ -66,6 +74,19 @@ SIGNATURES = {
 }
 W4Q_PROBE_SINK_WORDS = 65536
 
+# every function of w4a16q_layer.h (the layer around the core and its optimiser step)
+LAYER_SIGNATURES = {
+    "lsq_linear_fwd": (_INT, [_P, _I64, _P, _P, _I64, _I64, _P, _INT, _P, _P, _P, _P, _INT, _P, _SZ, _P]),
+    "lsq_linear_fwd_workspace_size": (_INT, [_I64, _I64, _I64, _P]),
+    "lsq_linear_bwd": (_INT, [_P, _I64, _P, _I64, _I64, _P, _INT, _INT, _P, _P, _P, _P, _P, _SZ, _P]),
+    "lsq_linear_bwd_workspace_size": (_INT, [_I64, _I64, _I64, _INT, _INT, _P]),
+    "w4a16_linear": (_INT, [_P, _I64, _P, _P, _I64, _I64, _P, _INT, _P, _P, _INT, _INT, _P, _SZ, _P]),
+    "newton_schulz": (_INT, [_P, _INT, _I64, _I64, _I64, _INT, _P, ctypes.c_double, _P, _INT, _P, _SZ, _P]),
+    "newton_schulz_workspace_size": (_INT, [_I64, _I64, _I64, _P]),
+    "muon_step": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P]),
+}
+W4Q_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
 
 class W4QError(RuntimeError):
     def __init__(self, fn: str, status: int):
@@ -85,7 +106,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it with `python -m w4a16_group_wise_amd.build` "
                 "(hipcc, gfx950).  There is no fallback implementation.")
         l = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **LAYER_SIGNATURES}.items():
             fn = getattr(l, name)
             fn.restype = res
             fn.argtypes = args

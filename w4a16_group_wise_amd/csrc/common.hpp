@@ -165,6 +165,13 @@ __device__ __forceinline__ void dma_x8(uint32_t lds, v4i32 rs, const int (&vo)[8
 
 __device__ __forceinline__ int lane_id() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)); }
 
+// Epilogue of a layer product (epilogue.hpp): act(sum + bias) + residual
+struct W4Epilogue {
+  const float* bias;  // [N] or null
+  const void* res;    // [M][N] of the output's type, or null
+  int act;            // w4q_act
+};
+
 }  // namespace w4q
 
 // Launchers (one per source file); return a w4q_status.
@@ -189,7 +196,8 @@ int w4q_launch_lsq_adam(float* w, float* scale, const float* g, int64_t d_out, i
                         float* m_w, float* v_w, float* m_s, float* v_s, const w4q_adam_params& hp,
                         float* ds_out, float* w_hat, hipStream_t s);
 int w4q_launch_gemv(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16,
-                    int64_t d_out, int64_t d_in, void* y, int y_dtype, hipStream_t s);
+                    int64_t d_out, int64_t d_in, void* y, int y_dtype, hipStream_t s,
+                    const w4q::W4Epilogue* ep = nullptr);
 bool w4q_gemv_group_fits(const w4q_gemv_problem* probs, int n);
 int w4q_launch_gemv_group(const w4q_gemv_problem* probs, int n, int y_dtype, hipStream_t s);
 // w_mode: 0 = exact weights (s16 * q), 1 = weights dequantized to bf16 (RNE of s16 * q)
@@ -212,7 +220,24 @@ int w4q_launch_gptq(const float* w, int64_t d_out, int64_t d_in, const float* h,
                     float damp, float* w_hat, int* info, void* ws, hipStream_t s);
 int w4q_launch_gemm(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16,
                     int64_t d_out, int64_t d_in, void* y, int y_dtype, int w_mode, void* ws,
-                    size_t ws_bytes, hipStream_t s);
+                    size_t ws_bytes, hipStream_t s, const w4q::W4Epilogue* ep = nullptr);
+int w4q_launch_lsq_fwd16(const float* w, const float* scale, int64_t d_out, int64_t d_in,
+                         uint16_t* w_hat, hipStream_t s);
+bool w4q_linear_fits(int64_t m, int64_t d_out, int64_t d_in, bool backward);
+size_t w4q_linear_fwd_workspace(int64_t m, int64_t d_out, int64_t d_in);
+size_t w4q_linear_bwd_workspace(int64_t m, int64_t d_out, int64_t d_in, int dy_f32, int act);
+int w4q_launch_linear_fwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,
+                          const float* bias, int act, const void* res, uint16_t* z, void* y, int y_dtype,
+                          void* ws, size_t ws_bytes, hipStream_t s);
+int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,
+                          const void* dy, int dy_f32, int act, const uint16_t* z, uint16_t* dx, float* dw,
+                          float* db, void* ws, hipStream_t s);
+bool w4q_ns_fits(int64_t batch, int64_t rows, int64_t cols);
+size_t w4q_ns_workspace(int64_t batch, int64_t rows, int64_t cols);
+bool w4q_ns_coeffs_ok(int steps, double a, double b, double c);
+int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64_t cols, int steps, float a,
+                  float b, float c, double eps, void* out, int out_dtype, float* m, float mu, int nesterov,
+                  float* w, float lr, float scale, float wd, void* ws, hipStream_t s);
 
 static inline int w4q_launch_status() {
   return hipGetLastError() == hipSuccess ? W4Q_OK : W4Q_EHIP;

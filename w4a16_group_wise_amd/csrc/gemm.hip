@@ -17,7 +17,7 @@
 // are XOR-swizzled in 16-byte chunks so fragment reads and tile writes are bank-conflict free.
 // Where this kernel would have fewer tiles than compute units, the exact product runs instead
 // on the stream-K kernel further down, with each weight split into two bf16-exact parts.
-#include "common.hpp"
+#include "epilogue.hpp"
 
 namespace w4q {
 namespace {
@@ -52,13 +52,14 @@ __device__ __forceinline__ u32x4 expand8(uint32_t word) {
 }
 
 // WM wavefronts along M (64 rows each) x WN along N; block tile (64 WM) x 128.
-template <int WM>
+template <int WM, bool kEpi>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_group_kernel(const uint16_t* __restrict__ x, int64_t M,
                                                           const uint8_t* __restrict__ packed,
                                                           const uint16_t* __restrict__ s16,
                                                           int64_t N, int64_t K,
                                                           void* __restrict__ y, int y_dtype,
-                                                          int64_t gn, int64_t tiles, int64_t per_xcd) {
+                                                          int64_t gn, int64_t tiles, int64_t per_xcd,
+                                                          const W4Epilogue ep) {
   constexpr int NT = 64 * WM * WN;  // threads
   constexpr int BM = 64 * WM;
   constexpr int BJ = BN * 4 / NT;   // B dwords (8 codes) per thread per group
@@ -185,10 +186,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_group_kernel(const uint16_t
       for (int r = 0; r < 16; ++r) {
         const int64_t row = m0 + wm * 64 + 32 * i + 8 * (r >> 2) + 4 * fh + (r & 3);
         if (row < M) {
+          const float v = kEpi ? apply_epilogue(ep, acc[i][j][r], row, col, N, y_dtype) : acc[i][j][r];
           if (y_dtype == 0)
-            reinterpret_cast<float*>(y)[row * N + col] = acc[i][j][r];
+            reinterpret_cast<float*>(y)[row * N + col] = v;
           else
-            reinterpret_cast<uint16_t*>(y)[row * N + col] = f32_to_bf16_bits(acc[i][j][r]);
+            reinterpret_cast<uint16_t*>(y)[row * N + col] = f32_to_bf16_bits(v);
         }
       }
     }
@@ -241,9 +243,10 @@ __device__ __forceinline__ int64_t gpart_off(int w, int i, int a, int lane) {
   return (int64_t)(((w * 8 + i) * 4 + a) * 256 + 4 * lane);
 }
 
-// Store one 32x32 accumulator block (rows row0.., columns col0..) of y.
+// Store one 32x32 accumulator block (rows row0.., columns col0..) of y, through the epilogue if kEpi.
+template <bool kEpi>
 __device__ __forceinline__ void gstore_block(void* __restrict__ y, int y_dtype, int M, int N, int row0, int col0,
-                                             const f32x16& v, int lane) {
+                                             const f32x16& acc, int lane, const W4Epilogue& ep) {
   const int col = col0 + (lane & 31);
   if (col >= N) return;
 #pragma unroll
@@ -251,10 +254,11 @@ __device__ __forceinline__ void gstore_block(void* __restrict__ y, int y_dtype, 
     const int row = row0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
     if (row >= M) continue;
     const int64_t o = (int64_t)row * N + col;
+    const float v = kEpi ? apply_epilogue(ep, acc[r], row, col, N, y_dtype) : acc[r];
     if (y_dtype == 0)
-      reinterpret_cast<float*>(y)[o] = v[r];
+      reinterpret_cast<float*>(y)[o] = v;
     else
-      reinterpret_cast<uint16_t*>(y)[o] = f32_to_bf16_bits(v[r]);
+      reinterpret_cast<uint16_t*>(y)[o] = f32_to_bf16_bits(v);
   }
 }
 
@@ -263,13 +267,13 @@ __device__ __forceinline__ void gstore_block(void* __restrict__ y, int y_dtype, 
 // |s - s_hi| <= 32 units of s's 11-bit significand): each part times a code (at most 3
 // significant bits) fits bf16's 8 bits exactly, so the two products per weight enter the fp32
 // sums unrounded.  Otherwise the weights are dequantized to bf16: w = bf16_RNE(s * q).
-template <bool kSplit>
+template <bool kSplit, bool kEpi>
 __global__ __launch_bounds__(kGThreads, 1) void gemm_dq_kernel(const uint16_t* __restrict__ x, int M,
                                                                 const uint8_t* __restrict__ packed,
                                                                 const uint16_t* __restrict__ s16, int N, int K,
                                                                 void* __restrict__ y, int y_dtype, int tn_count,
                                                                 int total, int chunk, int nblk, int per_xcd,
-                                                                float* __restrict__ ws) {
+                                                                float* __restrict__ ws, const W4Epilogue ep) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kGemmLds];
   const int G = K >> 5;
   const int lb = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
@@ -475,7 +479,7 @@ __global__ __launch_bounds__(kGThreads, 1) void gemm_dq_kernel(const uint16_t* _
     if (s0 == 0 && s1 == G) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        gstore_block(y, y_dtype, M, N, m0 + 32 * i, n0 + 32 * wid, acc[i], lane);
+        gstore_block<kEpi>(y, y_dtype, M, N, m0 + 32 * i, n0 + 32 * wid, acc[i], lane, ep);
         asm volatile("" ::: "memory");
       }
     } else {
@@ -496,9 +500,10 @@ __global__ __launch_bounds__(kGThreads, 1) void gemm_dq_kernel(const uint16_t* _
 // Tiles whose groups were spread over several workgroups: sum the partial tiles in the order of
 // their K ranges, then store.  One workgroup of 8 wavefronts per (tile, block row i); wavefront
 // w sums its own block (rows 32 i.., columns 32 w..).
+template <bool kEpi>
 __global__ __launch_bounds__(kGThreads) void gemm_fixup_kernel(void* __restrict__ y, int y_dtype, int M, int N,
                                                                int G, int tn_count, int chunk,
-                                                               const float* __restrict__ ws) {
+                                                               const float* __restrict__ ws, const W4Epilogue ep) {
   const int t = blockIdx.x >> 3;
   const int i = blockIdx.x & 7;
   const int first = static_cast<int>((int64_t)t * G / chunk);
@@ -520,7 +525,7 @@ __global__ __launch_bounds__(kGThreads) void gemm_fixup_kernel(void* __restrict_
       for (int e = 0; e < 4; ++e) v[4 * a + e] += q[e];
     }
   }
-  gstore_block(y, y_dtype, M, N, tm * GT + 32 * i, tn * GT + 32 * wid, v, lane);
+  gstore_block<kEpi>(y, y_dtype, M, N, tm * GT + 32 * i, tn * GT + 32 * wid, v, lane, ep);
 }
 
 // Schedule of one pass of the tiled kernel: stream-K ranges of `chunk` (tile, K-group)
@@ -569,30 +574,36 @@ DqPlan plan_dq(int64_t m, int64_t N, int64_t K, size_t ws_bytes) {
   return q;
 }
 
-int launch_dq_pass(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16, int64_t N,
-                    int64_t K, void* y, int y_dtype, bool exact, void* ws_ptr, size_t ws_bytes, hipStream_t s) {
-  const DqPlan p = plan_dq(m, N, K, ws_ptr != nullptr ? ws_bytes : 0);
-  if (p.total > 0x3FFFFFFF) return W4Q_EUNSUPPORTED;
-  float* ws = p.partial ? static_cast<float*>(ws_ptr) : nullptr;
-  const dim3 grid(static_cast<unsigned>(8 * p.per_xcd));
-  if (exact)
-    hipLaunchKernelGGL(gemm_dq_kernel<true>, grid, dim3(kGThreads), 0, s, x, static_cast<int>(m), packed, s16,
-                       static_cast<int>(N), static_cast<int>(K), y, y_dtype, static_cast<int>(p.tn_count),
-                       static_cast<int>(p.total), static_cast<int>(p.chunk), static_cast<int>(p.nblk),
-                       static_cast<int>(p.per_xcd), ws);
-  else
-    hipLaunchKernelGGL(gemm_dq_kernel<false>, grid, dim3(kGThreads), 0, s, x, static_cast<int>(m), packed, s16,
-                       static_cast<int>(N), static_cast<int>(K), y, y_dtype, static_cast<int>(p.tn_count),
-                       static_cast<int>(p.total), static_cast<int>(p.chunk), static_cast<int>(p.nblk),
-                       static_cast<int>(p.per_xcd), ws);
+template <bool kSplit, bool kEpi>
+int launch_dq_kernels(const DqPlan& p, const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16, int64_t N,
+                      int64_t K, void* y, int y_dtype, float* ws, const W4Epilogue& ep, hipStream_t s) {
+  hipLaunchKernelGGL((gemm_dq_kernel<kSplit, kEpi>), dim3(static_cast<unsigned>(8 * p.per_xcd)), dim3(kGThreads), 0, s, x,
+                     static_cast<int>(m), packed, s16, static_cast<int>(N), static_cast<int>(K), y, y_dtype,
+                     static_cast<int>(p.tn_count), static_cast<int>(p.total), static_cast<int>(p.chunk),
+                     static_cast<int>(p.nblk), static_cast<int>(p.per_xcd), ws, ep);
   int rc = w4q_launch_status();
   if (p.partial && rc == W4Q_OK) {
-    hipLaunchKernelGGL(gemm_fixup_kernel, dim3(static_cast<unsigned>(8 * p.tiles)), dim3(kGThreads), 0, s, y,
+    hipLaunchKernelGGL(gemm_fixup_kernel<kEpi>, dim3(static_cast<unsigned>(8 * p.tiles)), dim3(kGThreads), 0, s, y,
                        y_dtype, static_cast<int>(m), static_cast<int>(N), static_cast<int>(p.G),
-                       static_cast<int>(p.tn_count), static_cast<int>(p.chunk), ws);
+                       static_cast<int>(p.tn_count), static_cast<int>(p.chunk), ws, ep);
     rc = w4q_launch_status();
   }
   return rc;
+}
+
+// ep: null for the plain product
+int launch_dq_pass(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16, int64_t N,
+                    int64_t K, void* y, int y_dtype, bool exact, void* ws_ptr, size_t ws_bytes, hipStream_t s,
+                    const W4Epilogue* ep) {
+  const DqPlan p = plan_dq(m, N, K, ws_ptr != nullptr ? ws_bytes : 0);
+  if (p.total > 0x3FFFFFFF) return W4Q_EUNSUPPORTED;
+  float* ws = p.partial ? static_cast<float*>(ws_ptr) : nullptr;
+  const W4Epilogue none = {};
+  if (ep != nullptr)
+    return exact ? launch_dq_kernels<true, true>(p, x, m, packed, s16, N, K, y, y_dtype, ws, *ep, s)
+                 : launch_dq_kernels<false, true>(p, x, m, packed, s16, N, K, y, y_dtype, ws, *ep, s);
+  return exact ? launch_dq_kernels<true, false>(p, x, m, packed, s16, N, K, y, y_dtype, ws, none, s)
+               : launch_dq_kernels<false, false>(p, x, m, packed, s16, N, K, y, y_dtype, ws, none, s);
 }
 
 }  // namespace
@@ -611,7 +622,7 @@ static int64_t group_tiles(int64_t m, int64_t d_out, bool* big) {
 
 // exact weights, any shape: one K-group per step, scale applied per group on the vector ALUs
 static int launch_group(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16,
-                 int64_t d_out, int64_t d_in, void* y, int y_dtype, hipStream_t s) {
+                 int64_t d_out, int64_t d_in, void* y, int y_dtype, hipStream_t s, const W4Epilogue* ep) {
   if (d_in / kGroup > 0x7FFFFFFF) return W4Q_EUNSUPPORTED;
   const int64_t gn = (d_out + BN - 1) / BN;
   bool big;
@@ -619,12 +630,15 @@ static int launch_group(const uint16_t* x, int64_t m, const uint8_t* packed, con
   const int64_t per_xcd = (tiles + 7) / 8;
   if (8 * per_xcd > 0x7FFFFFFF) return W4Q_EUNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(8 * per_xcd));
+  const W4Epilogue none = {};
+  auto run = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, x, m, packed, s16, d_out, d_in, y, y_dtype, gn, tiles, per_xcd,
+                       ep != nullptr ? *ep : none);
+  };
   if (big)
-    hipLaunchKernelGGL(gemm_group_kernel<4>, grid, dim3(64 * 4 * WN), 0, s, x, m, packed, s16, d_out, d_in, y,
-                       y_dtype, gn, tiles, per_xcd);
+    ep != nullptr ? run(gemm_group_kernel<4, true>, 64 * 4 * WN) : run(gemm_group_kernel<4, false>, 64 * 4 * WN);
   else
-    hipLaunchKernelGGL(gemm_group_kernel<2>, grid, dim3(64 * 2 * WN), 0, s, x, m, packed, s16, d_out, d_in, y,
-                       y_dtype, gn, tiles, per_xcd);
+    ep != nullptr ? run(gemm_group_kernel<2, true>, 64 * 2 * WN) : run(gemm_group_kernel<2, false>, 64 * 2 * WN);
   return w4q_launch_status();
 }
 
@@ -655,23 +669,25 @@ size_t w4q_gemm_workspace(int64_t m, int64_t d_out, int64_t d_in, int w_mode) {
 
 int w4q_launch_gemm(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16,
                     int64_t d_out, int64_t d_in, void* y, int y_dtype, int w_mode, void* ws,
-                    size_t ws_bytes, hipStream_t s) {
+                    size_t ws_bytes, hipStream_t s, const W4Epilogue* ep) {
   if (w_mode == 0) {
     // exact weights: the per-group kernel while it has a tile for every compute unit; below
     // that, the stream-K tiled kernel with split weights (twice the matrix-core work, but the
     // K dimension spread over all compute units) when the caller's scratch holds its partial
     // tiles
     if (!exact_on_tiled(m, d_out, d_in) || ws == nullptr || ws_bytes < w4q_gemm_workspace(m, d_out, d_in, 0))
-      return launch_group(x, m, packed, s16, d_out, d_in, y, y_dtype, s);
+      return launch_group(x, m, packed, s16, d_out, d_in, y, y_dtype, s, ep);
   }
   if (!tiled_ok(d_out, d_in)) return W4Q_EUNSUPPORTED;
   const int64_t rows = pass_rows(d_in);
   const int64_t ob = y_dtype == 0 ? 4 : 2;
   for (int64_t r0 = 0; r0 < m; r0 += rows) {
     const int64_t mr = m - r0 < rows ? m - r0 : rows;
+    W4Epilogue e = ep != nullptr ? *ep : W4Epilogue{};
+    if (e.res != nullptr) e.res = static_cast<const uint8_t*>(e.res) + r0 * d_out * ob;
     const int rc = launch_dq_pass(x + r0 * d_in, mr, packed, s16, d_out, d_in,
                                   static_cast<uint8_t*>(y) + r0 * d_out * ob, y_dtype, w_mode == 0, ws,
-                                  ws_bytes, s);
+                                  ws_bytes, s, ep != nullptr ? &e : nullptr);
     if (rc != W4Q_OK) return rc;
   }
   return W4Q_OK;

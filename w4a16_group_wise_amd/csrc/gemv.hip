@@ -28,7 +28,7 @@
 // codes, scales and activations are loaded while the current chunk is being reduced.
 #include <atomic>
 
-#include "common.hpp"
+#include "epilogue.hpp"
 
 namespace w4q {
 namespace {
@@ -261,12 +261,12 @@ struct MmaBatch {
 
 // kMmaTiles: 16-row tiles of W per workgroup (1 or 2); kWaves: wavefronts per workgroup (8, or
 // 16 for long rows, where each still gets two batches or more)
-template <bool kVecScales, int kMmaTiles, int kWaves = kMmaWaves>
+template <bool kVecScales, int kMmaTiles, int kWaves = kMmaWaves, bool kEpi = false>
 __global__ __launch_bounds__(kWaves * 64) void gemv_mma_kernel(const uint16_t* __restrict__ x, int m_rows,
                                                                   const uint8_t* __restrict__ packed,
                                                                   const uint16_t* __restrict__ s16,
                                                                   int64_t d_out, int64_t d_in,
-                                                                  void* __restrict__ y, int y_dtype) {
+                                                                  void* __restrict__ y, int y_dtype, const W4Epilogue ep) {
   __shared__ float part[kWaves][kMmaTiles][4][64];
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -401,6 +401,7 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_mma_kernel(const uint16_t* _
     for (int w = 0; w < kWaves; ++w) v += part[w][t][m & 3][src];
     const int64_t n = nbase + 16 * t + c;
     if (m < m_rows && n < d_out) {
+      if constexpr (kEpi) v = apply_epilogue(ep, v, m, n, d_out, y_dtype);
       if (y_dtype == 0)
         reinterpret_cast<float*>(y)[m * d_out + n] = v;
       else
@@ -498,8 +499,8 @@ constexpr int stream_threads() { return kLut ? 512 : 256; }
 // reads of that problem's entries.  (Staging the table through LDS first put a barrier and an LDS
 // round trip before the first code load: per-phase decode pass of the 36-layer stack 1262 ->
 // 1205 us without it.)
-template <int LPR, int RS, bool kLut>
-__global__ __launch_bounds__(stream_threads<kLut>()) void gemv_stream_kernel(const GroupArgs t) {
+template <int LPR, int RS, bool kLut, bool kEpi>
+__global__ __launch_bounds__(stream_threads<kLut>()) void gemv_stream_kernel(const GroupArgs t, const W4Epilogue ep) {
   constexpr int kStreamThreads = stream_threads<kLut>();
   __shared__ uint32_t lut[kLut ? 256 * 64 : 1];
   constexpr int RPS = 64 / LPR;
@@ -604,6 +605,7 @@ __global__ __launch_bounds__(stream_threads<kLut>()) void gemv_stream_kernel(con
     }
   };
   auto store = [&](void* y, int64_t row, float v) {
+    if constexpr (kEpi) v = apply_epilogue(ep, v, 0, row, 0, ydt);  // one row: the output's index is its column
     if (ydt == 0)
       global_ptr(reinterpret_cast<float*>(y))[row] = v;
     else
@@ -769,7 +771,7 @@ namespace {
 // compute unit, queried once per device and kernel.
 int resident_grid(const void* kernel, int slot, int threads = kThreads) {
   constexpr int kDevices = 64;
-  static std::atomic<int> cache[kDevices][24];
+  static std::atomic<int> cache[kDevices][28];
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
   if (dev < kDevices) {
@@ -784,29 +786,29 @@ int resident_grid(const void* kernel, int slot, int threads = kThreads) {
   return v;
 }
 
-template <int LPR, int RS, bool kLut>
-int launch_stream(const GroupArgs& a, int64_t items, int slot, hipStream_t s) {
+template <int LPR, int RS, bool kLut, bool kEpi>
+int launch_stream(const GroupArgs& a, int64_t items, int slot, hipStream_t s, const W4Epilogue& ep) {
   constexpr int nt = stream_threads<kLut>();
-  auto* k = &gemv_stream_kernel<LPR, RS, kLut>;
+  auto* k = &gemv_stream_kernel<LPR, RS, kLut, kEpi>;
   const int res = resident_grid(reinterpret_cast<const void*>(k), slot, nt);
   if (res <= 0) return W4Q_EHIP;
   const int64_t need = (items + nt / 64 - 1) / (nt / 64);
   const unsigned grid = static_cast<unsigned>(need < res ? need : res);
-  hipLaunchKernelGGL(k, dim3(grid), dim3(nt), 0, s, a);
+  hipLaunchKernelGGL(k, dim3(grid), dim3(nt), 0, s, a, ep);
   return w4q_launch_status();
 }
 
-template <bool kLut>
-int launch_stream_lpr(const GroupArgs& a, int64_t items, int lpr, hipStream_t s) {
-  constexpr int base = kLut ? 0 : 7;  // resident-grid cache slots
+template <bool kLut, bool kEpi>
+int launch_stream_lpr(const GroupArgs& a, int64_t items, int lpr, hipStream_t s, const W4Epilogue& ep) {
+  constexpr int base = (kLut ? 0 : 7) + (kEpi ? 14 : 0);  // resident-grid cache slots
   switch (lpr) {
-    case 64: return launch_stream<64, 4, kLut>(a, items, base + 0, s);
-    case 32: return launch_stream<32, 4, kLut>(a, items, base + 1, s);
-    case 16: return launch_stream<16, 4, kLut>(a, items, base + 2, s);
-    case 8: return launch_stream<8, 4, kLut>(a, items, base + 3, s);
-    case 4: return launch_stream<4, 4, kLut>(a, items, base + 4, s);
-    case 2: return launch_stream<2, 4, kLut>(a, items, base + 5, s);
-    default: return launch_stream<1, 4, kLut>(a, items, base + 6, s);
+    case 64: return launch_stream<64, 4, kLut, kEpi>(a, items, base + 0, s, ep);
+    case 32: return launch_stream<32, 4, kLut, kEpi>(a, items, base + 1, s, ep);
+    case 16: return launch_stream<16, 4, kLut, kEpi>(a, items, base + 2, s, ep);
+    case 8: return launch_stream<8, 4, kLut, kEpi>(a, items, base + 3, s, ep);
+    case 4: return launch_stream<4, 4, kLut, kEpi>(a, items, base + 4, s, ep);
+    case 2: return launch_stream<2, 4, kLut, kEpi>(a, items, base + 5, s, ep);
+    default: return launch_stream<1, 4, kLut, kEpi>(a, items, base + 6, s, ep);
   }
 }
 
@@ -832,7 +834,9 @@ int64_t chunk_items(const w4q_gemv_problem* probs, int cnt, int lpr) {
 // ones take the byte-select conversion, whose workgroups start streaming at once.  (Measured per
 // launch, 4096x4096 repeated: 5.4 us with the table, 4.0 us without; 24576x4096: 12.3 vs 13.9 us;
 // all 252 linears of the 36-layer stack in 64-problem launches: 699 vs 836 us.)
-int launch_group_chunk(const w4q_gemv_problem* probs, int cnt, int y_dtype, hipStream_t s) {
+// ep: the epilogue of a single problem, or null.
+int launch_group_chunk(const w4q_gemv_problem* probs, int cnt, int y_dtype, hipStream_t s,
+                       const W4Epilogue* ep = nullptr) {
   GroupArgs a = {};
   const int lpr = chunk_lpr(probs, cnt);
   const int rows_per_item = 4 * (64 / lpr);
@@ -852,53 +856,67 @@ int launch_group_chunk(const w4q_gemv_problem* probs, int cnt, int y_dtype, hipS
   a.first[cnt] = static_cast<int>(items);
   a.n = cnt;
   a.y_dtype = y_dtype;
-  if (bytes >= (int64_t(48) << 20) && items >= 4096) return launch_stream_lpr<true>(a, items, lpr, s);
-  return launch_stream_lpr<false>(a, items, lpr, s);
+  const bool lut = bytes >= (int64_t(48) << 20) && items >= 4096;
+  if (ep != nullptr)
+    return lut ? launch_stream_lpr<true, true>(a, items, lpr, s, *ep) : launch_stream_lpr<false, true>(a, items, lpr, s, *ep);
+  const W4Epilogue none = {};
+  return lut ? launch_stream_lpr<true, false>(a, items, lpr, s, none) : launch_stream_lpr<false, false>(a, items, lpr, s, none);
+}
+
+}  // namespace
+}  // namespace w4q
+
+namespace w4q {
+namespace {
+
+// 2..16 activation rows on the matrix cores
+template <bool kEpi>
+int launch_mma(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16, int64_t d_out, int64_t d_in,
+               void* y, int y_dtype, hipStream_t s, const W4Epilogue& ep) {
+  const int tiles = d_out < 8192 ? 1 : 2;
+  const int64_t blocks = (d_out + 16 * tiles - 1) / (16 * tiles);
+  if (blocks > 0x7FFFFFFF) return W4Q_EUNSUPPORTED;
+  const bool vec = (d_in / kGroup) % kMmaBatch == 0;
+  auto run = [&](auto kernel, int waves) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(waves * 64), 0, s, x, static_cast<int>(m), packed,
+                       s16, d_out, d_in, y, y_dtype, ep);
+  };
+  // 16 wavefronts per workgroup (twice the loads in flight per compute unit) on long rows with
+  // one tile per workgroup: d_in >= 8192 gives each wavefront two 8-group batches or more
+  // (measured at 4096x12288, M = 2..8: 17.6 -> 15.5 us at M = 2; no gain at M = 16, and a loss
+  // where the wavefronts get one batch each)
+  if (tiles == 1 && d_in >= 8192 && m <= 8) {
+    if (vec)
+      run(gemv_mma_kernel<true, 1, 16, kEpi>, 16);
+    else
+      run(gemv_mma_kernel<false, 1, 16, kEpi>, 16);
+  } else if (vec && tiles == 2) {
+    run(gemv_mma_kernel<true, 2, kMmaWaves, kEpi>, kMmaWaves);
+  } else if (vec) {
+    run(gemv_mma_kernel<true, 1, kMmaWaves, kEpi>, kMmaWaves);
+  } else if (tiles == 2) {
+    run(gemv_mma_kernel<false, 2, kMmaWaves, kEpi>, kMmaWaves);
+  } else {
+    run(gemv_mma_kernel<false, 1, kMmaWaves, kEpi>, kMmaWaves);
+  }
+  return w4q_launch_status();
 }
 
 }  // namespace
 }  // namespace w4q
 
 // 2..16 activation rows: one matrix-core launch.  A single row takes the stream kernel (as a
-// one-problem group) when its sizes fit 32 bits, else the vector kernel.
+// one-problem group) when its sizes fit 32 bits, else the vector kernel (which has no epilogue).
 int w4q_launch_gemv(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16,
-                    int64_t d_out, int64_t d_in, void* y, int y_dtype, hipStream_t s) {
+                    int64_t d_out, int64_t d_in, void* y, int y_dtype, hipStream_t s, const W4Epilogue* ep) {
   if (m >= 2 && m <= 16) {
-    const int tiles = d_out < 8192 ? 1 : 2;
-    const int64_t blocks = (d_out + 16 * tiles - 1) / (16 * tiles);
-    if (blocks > 0x7FFFFFFF) return W4Q_EUNSUPPORTED;
-    const bool vec = (d_in / kGroup) % kMmaBatch == 0;
-    const dim3 grid(static_cast<unsigned>(blocks)), block(kMmaWaves * 64);
-    const int mr = static_cast<int>(m);
-    // 16 wavefronts per workgroup (twice the loads in flight per compute unit) on long rows with
-    // one tile per workgroup: d_in >= 8192 gives each wavefront two 8-group batches or more
-    // (measured at 4096x12288, M = 2..8: 17.6 -> 15.5 us at M = 2; no gain at M = 16, and a loss
-    // where the wavefronts get one batch each)
-    if (tiles == 1 && d_in >= 8192 && m <= 8) {
-      const dim3 block16(16 * 64);
-      if (vec)
-        hipLaunchKernelGGL((gemv_mma_kernel<true, 1, 16>), grid, block16, 0, s, x, mr, packed, s16, d_out, d_in, y,
-                           y_dtype);
-      else
-        hipLaunchKernelGGL((gemv_mma_kernel<false, 1, 16>), grid, block16, 0, s, x, mr, packed, s16, d_out, d_in, y,
-                           y_dtype);
-      return w4q_launch_status();
-    }
-    if (vec && tiles == 2)
-      hipLaunchKernelGGL((gemv_mma_kernel<true, 2>), grid, block, 0, s, x, mr, packed, s16, d_out, d_in, y, y_dtype);
-    else if (vec)
-      hipLaunchKernelGGL((gemv_mma_kernel<true, 1>), grid, block, 0, s, x, mr, packed, s16, d_out, d_in, y, y_dtype);
-    else if (tiles == 2)
-      hipLaunchKernelGGL((gemv_mma_kernel<false, 2>), grid, block, 0, s, x, mr, packed, s16, d_out, d_in, y, y_dtype);
-    else
-      hipLaunchKernelGGL((gemv_mma_kernel<false, 1>), grid, block, 0, s, x, mr, packed, s16, d_out, d_in, y, y_dtype);
-    return w4q_launch_status();
+    if (ep != nullptr) return launch_mma<true>(x, m, packed, s16, d_out, d_in, y, y_dtype, s, *ep);
+    return launch_mma<false>(x, m, packed, s16, d_out, d_in, y, y_dtype, s, W4Epilogue{});
   }
-  // one activation row: the persistent stream kernel, or the plain vector kernel when the
-  // stream's 32-bit offsets do not cover the shape
   const w4q_gemv_problem one = {x, packed, s16, y, d_out, d_in};
   if (d_out <= 0x7FFFFFFF && d_in <= (1 << 24) && w4q_gemv_group_fits(&one, 1))
-    return launch_group_chunk(&one, 1, y_dtype, s);
+    return launch_group_chunk(&one, 1, y_dtype, s, ep);
+  if (ep != nullptr) return W4Q_EUNSUPPORTED;
   return launch_mt<1>(x, 1, packed, s16, d_out, d_in, y, y_dtype, s);
 }
 

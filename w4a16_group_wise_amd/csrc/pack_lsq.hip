@@ -113,6 +113,27 @@ __global__ __launch_bounds__(kThreads) void lsq_fwd_kernel(const float* __restri
   *reinterpret_cast<f32x4*>(w_hat + e0 + 4) = f32x4{d * c[4], d * c[5], d * c[6], d * c[7]};
 }
 
+// The same forward with the result in the 16-bit activation format, bf16_RNE(fl32(D * code(w, D))),
+// for the layer's product (linear.hip): 6 B per weight + 4 per group, HBM bound.
+__global__ __launch_bounds__(kThreads) void lsq_fwd16_kernel(const float* __restrict__ w,
+                                                             const float* __restrict__ scale, int64_t n8,
+                                                             uint16_t* __restrict__ w_hat) {
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= n8) return;
+  const int64_t e0 = t * kPer;
+  const float d = scale[e0 / kGroup];
+  const f32x4 a = *reinterpret_cast<const f32x4*>(w + e0);
+  const f32x4 b = *reinterpret_cast<const f32x4*>(w + e0 + 4);
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float c[8];
+  fast_codes(v, d, c);
+  uint32_t h[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    h[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{d * c[2 * p], d * c[2 * p + 1]}, bf16x2));
+  *reinterpret_cast<u32x4*>(w_hat + e0) = u32x4{h[0], h[1], h[2], h[3]};
+}
+
 // [blog] section 3 backward.  m = [-8 D <= w <= 7 D] (signs from fma, exact);
 // grad_w = G m;  f = q - (w / D) m;  grad_scale = gs * sum_group G f.
 template <bool kFwd>
@@ -252,6 +273,13 @@ int w4q_launch_lsq_fwd(const float* w, const float* scale, int64_t d_out, int64_
   const int64_t n8 = d_out * d_in / kPer;
   hipLaunchKernelGGL(lsq_fwd_kernel, dim3(blocks_for(n8)), dim3(kThreads), 0, s, w, scale, n8,
                      w_hat);
+  return w4q_launch_status();
+}
+
+int w4q_launch_lsq_fwd16(const float* w, const float* scale, int64_t d_out, int64_t d_in,
+                         uint16_t* w_hat, hipStream_t s) {
+  const int64_t n8 = d_out * d_in / kPer;
+  hipLaunchKernelGGL(lsq_fwd16_kernel, dim3(blocks_for(n8)), dim3(kThreads), 0, s, w, scale, n8, w_hat);
   return w4q_launch_status();
 }
 

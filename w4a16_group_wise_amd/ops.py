@@ -56,7 +56,8 @@ def _workspace(query: str, sizes, device, workspace: Optional[torch.Tensor]):
 
 def workspace_size(op: str, *sizes) -> int:
     """Scratch bytes: op in ("quant_hessian", "w4a16_gemm", "w4a16_gemm_dq", "per_channel", "joint",
-    "gptq") with (n_tok, d), (m, d_out, d_in) or (d_out, d_in) as the C query takes them."""
+    "gptq", "lsq_linear_fwd", "lsq_linear_bwd", "newton_schulz") with (n_tok, d), (m, d_out, d_in),
+    (d_out, d_in), (m, d_out, d_in, grad_y dtype, act) or (batch, rows, cols) as the C query takes them."""
     n = ctypes.c_size_t(0)
     check(op + "_workspace_size", getattr(lib(), op + "_workspace_size")(*sizes, ctypes.byref(n)))
     return n.value
@@ -367,6 +368,210 @@ def quant_gptq(w: torch.Tensor, h: torch.Tensor, scale: torch.Tensor, damp: floa
     check("quant_gptq", lib().quant_gptq(w.data_ptr(), d_out, d_in, h.data_ptr(), h.shape[1], scale.data_ptr(),
                                          float(damp), w_hat.data_ptr(), info.data_ptr(), wp, wb, _stream(w)))
     return w_hat, info
+
+
+# ------------------------------------------------------------- the layer and its optimiser step
+NS_COEFFS = (3.4445, -4.7750, 2.0315)  # the published Muon coefficients
+
+
+def _act(act: str) -> int:
+    from ._lib import W4Q_ACTS
+    if act not in W4Q_ACTS:
+        raise ValueError(f"act must be one of {', '.join(W4Q_ACTS)}, got {act!r}")
+    return W4Q_ACTS[act]
+
+
+def _dtype_code(dtype: torch.dtype, name: str) -> int:
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return 0 if dtype == torch.float32 else 1
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(x: torch.Tensor, name: str) -> Tuple[int, int]:
+    _need(x, name, torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {x.dim()}")
+    return x.shape[0], x.shape[1]
+
+
+def _no_overlap(pairs) -> None:
+    """Each pair ((tensor, name), (tensor, name)) must not share memory."""
+    for (a, an), (b, bn) in pairs:
+        if a is None or b is None:
+            continue
+        a0, b0 = a.data_ptr(), b.data_ptr()
+        if a0 < b0 + b.numel() * b.element_size() and b0 < a0 + a.numel() * a.element_size():
+            raise ValueError(f"{an} and {bn} overlap")
+
+
+def _epilogue(m, d_out, dtype, device, bias, residual) -> None:
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (d_out,), device)
+    if residual is not None:
+        _need(residual, "residual", dtype, (m, d_out), device)
+
+
+def lsq_linear_fwd(x: torch.Tensor, w: Optional[torch.Tensor], scale: Optional[torch.Tensor], *,
+                   bias: Optional[torch.Tensor] = None, act: str = "none",
+                   residual: Optional[torch.Tensor] = None, w_hat: Optional[torch.Tensor] = None,
+                   with_z: bool = False, out_dtype: torch.dtype = torch.bfloat16,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """y = act(x W^T + bias) + residual with W = bf16(scale * code(w, scale)), for bf16 x [m][d_in],
+    fp32 w [d_out][d_in] and scale [d_out][G].  -> (y [m][d_out], w_hat bf16 [d_out][d_in], z bf16
+    [m][d_out] | None).  act: "none", "relu", "gelu" or "silu"; bias fp32 [d_out]; residual of y's type
+    (may be `out` itself); with_z keeps the pre-activation for lsq_linear_bwd.  With w and scale None,
+    w_hat is taken as given (further micro-batches on the same weights)."""
+    m, d_in = _rows(x, "x")
+    a, ydt = _act(act), _dtype_code(out_dtype, "out_dtype")
+    if (w is None) != (scale is None):
+        raise ValueError("w and scale are given together, or neither")
+    if w is not None:
+        _need(w, "w", torch.float32, device=x.device)
+        if w.dim() != 2 or w.shape[1] != d_in:
+            raise ValueError(f"w must be [d_out][{d_in}], got {tuple(w.shape)}")
+        d_out = w.shape[0]
+        _need(scale, "scale", torch.float32, (d_out, d_in // W4Q_GROUP), x.device)
+        w_hat = _out(w_hat, "w_hat", (d_out, d_in), torch.bfloat16, x.device)
+    else:
+        if w_hat is None:
+            raise ValueError("w and scale, or w_hat, must be given")
+        _need(w_hat, "w_hat", torch.bfloat16, device=x.device)
+        if w_hat.dim() != 2 or w_hat.shape[1] != d_in:
+            raise ValueError(f"w_hat must be [d_out][{d_in}], got {tuple(w_hat.shape)}")
+        d_out = w_hat.shape[0]
+    _epilogue(m, d_out, out_dtype, x.device, bias, residual)
+    with torch.cuda.device(x.device):
+        y = _out(out, "y", (m, d_out), out_dtype, x.device)
+        z = torch.empty((m, d_out), dtype=torch.bfloat16, device=x.device) if with_z else None
+        if out is not None:
+            _no_overlap((((y, "out"), (t, n)) for t, n in ((x, "x"), (w, "w"), (w_hat, "w_hat"))))
+        wp, wb, _keep = _workspace("lsq_linear_fwd_workspace_size", (m, d_out, d_in), x.device, workspace)
+        check("lsq_linear_fwd", lib().lsq_linear_fwd(
+            x.data_ptr(), m, _ptr(w), _ptr(scale), d_out, d_in, _ptr(bias), a, _ptr(residual), w_hat.data_ptr(),
+            _ptr(z), y.data_ptr(), ydt, wp, wb, _stream(x)))
+    return y, w_hat, z
+
+
+def lsq_linear_bwd(x: torch.Tensor, w_hat: torch.Tensor, grad_y: torch.Tensor, *, act: str = "none",
+                   z: Optional[torch.Tensor] = None, with_bias: bool = False, with_x: bool = True,
+                   with_w: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Gradients of lsq_linear_fwd from its bf16 x, w_hat and (unless act is "none") z, and grad_y
+    [m][d_out] (bf16 or fp32).  -> (grad_x bf16 [m][d_in] | None, grad_w_hat fp32 [d_out][d_in] | None,
+    grad_bias fp32 [d_out] | None); grad_w_hat is what lsq_bwd and lsq_adam_step take.  The residual's
+    gradient is grad_y."""
+    m, d_in = _rows(x, "x")
+    _need(w_hat, "w_hat", torch.bfloat16, device=x.device)
+    if w_hat.dim() != 2 or w_hat.shape[1] != d_in:
+        raise ValueError(f"w_hat must be [d_out][{d_in}], got {tuple(w_hat.shape)}")
+    d_out, a = w_hat.shape[0], _act(act)
+    if not isinstance(grad_y, torch.Tensor):
+        raise TypeError("grad_y must be a torch.Tensor")
+    gdt = _dtype_code(grad_y.dtype, "grad_y")
+    _need(grad_y, "grad_y", grad_y.dtype, (m, d_out), x.device)
+    if a != 0:
+        if z is None:
+            raise ValueError(f"act={act!r} needs z")
+        _need(z, "z", torch.bfloat16, (m, d_out), x.device)
+    if not (with_x or with_w or with_bias):
+        raise ValueError("no gradient asked for")
+    with torch.cuda.device(x.device):
+        gx = torch.empty((m, d_in), dtype=torch.bfloat16, device=x.device) if with_x else None
+        gw = torch.empty((d_out, d_in), dtype=torch.float32, device=x.device) if with_w else None
+        gb = torch.empty(d_out, dtype=torch.float32, device=x.device) if with_bias else None
+        wp, wb, _keep = _workspace("lsq_linear_bwd_workspace_size", (m, d_out, d_in, gdt, a), x.device, workspace)
+        check("lsq_linear_bwd", lib().lsq_linear_bwd(
+            x.data_ptr(), m, w_hat.data_ptr(), d_out, d_in, grad_y.data_ptr(), gdt, a, _ptr(z) if a != 0 else None,
+            _ptr(gx), _ptr(gw), _ptr(gb), wp, wb, _stream(x)))
+    return gx, gw, gb
+
+
+def w4a16_linear(x: torch.Tensor, packed: torch.Tensor, scale_f16: torch.Tensor, *,
+                 bias: Optional[torch.Tensor] = None, act: str = "none", residual: Optional[torch.Tensor] = None,
+                 dequant_bf16: bool = False, out_dtype: torch.dtype = torch.float32,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The deployed layer: y [m][d_out] = act(x W_hat^T + bias) + residual on packed codes, in one launch
+    for up to 16 rows; W_hat as w4a16_gemm (exact), or as w4a16_gemm_dq with dequant_bf16.  bias fp32
+    [d_out]; residual of y's type (may be `out` itself)."""
+    m, d_in = _rows(x, "x")
+    _need(packed, "packed", torch.uint8, device=x.device)
+    if packed.dim() != 2 or packed.shape[1] * 2 != d_in:
+        raise ValueError(f"packed must be [d_out][{d_in // 2}], got {tuple(packed.shape)}")
+    d_out = packed.shape[0]
+    _need(scale_f16, "scale_f16", torch.float16, (d_out, d_in // W4Q_GROUP), x.device)
+    a, ydt = _act(act), _dtype_code(out_dtype, "out_dtype")
+    _epilogue(m, d_out, out_dtype, x.device, bias, residual)
+    with torch.cuda.device(x.device):
+        y = _out(out, "y", (m, d_out), out_dtype, x.device)
+        if out is not None:
+            _no_overlap((((y, "out"), (t, n)) for t, n in ((x, "x"), (packed, "packed"), (scale_f16, "scale_f16"))))
+        query = "w4a16_gemm_dq_workspace_size" if dequant_bf16 else "w4a16_gemm_workspace_size"
+        wp, wb, _keep = _workspace(query, (m, d_out, d_in), x.device, workspace)
+        check("w4a16_linear", lib().w4a16_linear(
+            x.data_ptr(), m, packed.data_ptr(), scale_f16.data_ptr(), d_out, d_in, _ptr(bias), a, _ptr(residual),
+            y.data_ptr(), ydt, 1 if dequant_bf16 else 0, wp, wb, _stream(x)))
+    return y
+
+
+def _matrices(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(batch, rows, cols) of a [rows][cols] or [batch][rows][cols] tensor."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [rows][cols] or [batch][rows][cols], got {tuple(t.shape)}")
+    return (1 if t.dim() == 2 else t.shape[0]), t.shape[-2], t.shape[-1]
+
+
+def newton_schulz(g: torch.Tensor, *, steps: int = 5, coeffs=NS_COEFFS, eps: float = 1e-7,
+                  out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """g [rows][cols] or [batch][rows][cols] (fp32 or bf16) orthogonalised by `steps` Newton-Schulz
+    products: X = g / (||g||_F + eps), then X = a X + (b A + c A A) X with A = X X^T.  out_dtype: fp32
+    (default) or bf16; `out` may be g itself."""
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch.Tensor")
+    gdt = _dtype_code(g.dtype, "g")
+    _need(g, "g", g.dtype)
+    b, r, c = _matrices(g, "g")
+    odt = out_dtype if out_dtype is not None else (torch.float32 if out is None else out.dtype)
+    o = _dtype_code(odt, "out_dtype")
+    if len(coeffs) != 3:
+        raise ValueError("coeffs must be (a, b, c)")
+    with torch.cuda.device(g.device):
+        y = _out(out, "out", tuple(g.shape), odt, g.device)
+        if out is not None and not (y.data_ptr() == g.data_ptr() and y.dtype == g.dtype):
+            _no_overlap((((y, "out"), (g, "g")),))
+        wp, wb, _keep = _workspace("newton_schulz_workspace_size", (b, r, c), g.device, workspace)
+        check("newton_schulz", lib().newton_schulz(
+            g.data_ptr(), gdt, b, r, c, int(steps), (ctypes.c_float * 3)(*coeffs), float(eps), y.data_ptr(), o, wp, wb,
+            _stream(g)))
+    return y
+
+
+def muon_step(w: torch.Tensor, grad: torch.Tensor, m: torch.Tensor, *, lr: float, momentum: float = 0.95,
+              nesterov: bool = True, weight_decay: float = 0.0, update_scale: Optional[float] = None,
+              steps: int = 5, coeffs=NS_COEFFS, eps: float = 1e-7, workspace: Optional[torch.Tensor] = None) -> None:
+    """One Muon step in place on fp32 w, with momentum buffer m, for [rows][cols] or [batch][rows][cols]:
+    m = momentum m + grad;  u = grad + momentum m (nesterov) or m;
+    w = w - lr (update_scale newton_schulz(u) + weight_decay w).
+    update_scale defaults to sqrt(max(1, rows / cols)).  grad is e.g. lsq_bwd's grad_w."""
+    from ._lib import MuonParams
+    _need(w, "w", torch.float32)
+    b, r, c = _matrices(w, "w")
+    _need(grad, "grad", torch.float32, tuple(w.shape), w.device)
+    _need(m, "m", torch.float32, tuple(w.shape), w.device)
+    _no_overlap((((w, "w"), (grad, "grad")), ((w, "w"), (m, "m")), ((grad, "grad"), (m, "m"))))
+    if len(coeffs) != 3:
+        raise ValueError("coeffs must be (a, b, c)")
+    if update_scale is None:
+        update_scale = max(1.0, r / max(c, 1)) ** 0.5
+    hp = MuonParams(lr, momentum, weight_decay, update_scale, (ctypes.c_float * 3)(*coeffs), 1 if nesterov else 0,
+                    int(steps), float(eps))
+    with torch.cuda.device(w.device):
+        wp, wb, _keep = _workspace("newton_schulz_workspace_size", (b, r, c), w.device, workspace)
+        check("muon_step", lib().muon_step(w.data_ptr(), grad.data_ptr(), m.data_ptr(), b, r, c, ctypes.byref(hp), wp,
+                                           wb, _stream(w)))
 
 
 class GemvGroupPlan:
