@@ -10,13 +10,20 @@ namespace w4q {
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
 __device__ __forceinline__ float bf16_val(uint16_t b) { return __builtin_bit_cast(float, static_cast<uint32_t>(b) << 16); }
 
+// 1 / (1 + exp(-z)) by the hardware's 2^x and reciprocal (each within one last place): the exponent's
+// rounding puts |z| 2^-24 on exp(-z), which reaches the result times 1 - sigmoid, so silu and its
+// derivative stay within a few 2^-24 of |z| + 1.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+
 // act(z) in fp32.  gelu is z Phi(z) with Phi by the complementary error function (no cancellation
 // for negative z); relu keeps NaN.
 __device__ __forceinline__ float act_fwd(float z, int act) {
   switch (act) {
     case W4Q_ACT_RELU: return z <= 0.0f ? 0.0f : z;
     case W4Q_ACT_GELU: return z * 0.5f * erfcf(z * -0.70710678118654752f);
-    case W4Q_ACT_SILU: return z / (1.0f + expf(-z));
+    case W4Q_ACT_SILU: return z * sigmoid(z);
     default: return z;
   }
 }
@@ -28,24 +35,66 @@ __device__ __forceinline__ float act_grad(float z, int act) {
     case W4Q_ACT_GELU:
       return 0.5f * erfcf(z * -0.70710678118654752f) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
     case W4Q_ACT_SILU: {
-      const float s = 1.0f / (1.0f + expf(-z));
+      const float s = sigmoid(z);
       return s * (1.0f + z * (1.0f - s));
     }
     default: return 1.0f;
   }
 }
 
-// the rest of an output after its sum: the residual has y's type (y_dtype 0 fp32, 1 bf16)
-__device__ __forceinline__ float finish_output(const W4Epilogue& e, float z, int64_t o, int y_dtype) {
-  float v = act_fwd(z, e.act);
+__device__ __forceinline__ float apply_epilogue(const W4Epilogue& e, float v, int64_t row, int64_t col, int64_t n,
+                                                int y_dtype) {
+  if (e.bias != nullptr) v += e.bias[col];
+  v = act_fwd(v, e.act);
+  const int64_t o = row * n + col;
   if (e.res != nullptr)
     v += y_dtype == 0 ? static_cast<const float*>(e.res)[o] : bf16_val(static_cast<const uint16_t*>(e.res)[o]);
   return v;
 }
-__device__ __forceinline__ float apply_epilogue(const W4Epilogue& e, float v, int64_t row, int64_t col, int64_t n,
-                                                int y_dtype) {
-  if (e.bias != nullptr) v += e.bias[col];
-  return finish_output(e, v, row * n + col, y_dtype);
+
+// 8 consecutive values as fp32 from fp32 (dtype 0) or bf16 (1) at element o, and back; 16-byte aligned
+__device__ __forceinline__ void unpack8(const u32x4& a, const u32x4& b, int dtype, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (dtype == 0) {
+      const uint32_t u = a[i], w = b[i];  // (a bit cast of a vector's element itself takes element 0)
+      v[i] = __builtin_bit_cast(float, u);
+      v[4 + i] = __builtin_bit_cast(float, w);
+    } else {
+      v[2 * i] = bf16_lo(a[i]);
+      v[2 * i + 1] = bf16_hi(a[i]);
+    }
+  }
+}
+__device__ __forceinline__ void load8(const void* p, int64_t o, int dtype, u32x4& a, u32x4& b) {
+  if (dtype == 0) {
+    a = *reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + o);
+    b = *reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + o + 4);
+  } else {
+    a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + o);
+  }
+}
+__device__ __forceinline__ u32x4 pack_bf16(const float (&v)[8]) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * i], v[2 * i + 1]}, bf16x2));
+  return u32x4{h[0], h[1], h[2], h[3]};
+}
+__device__ __forceinline__ void store8(void* p, int64_t o, int dtype, const float (&v)[8]) {
+  if (dtype == 0) {
+    float* f = static_cast<float*>(p) + o;
+    *reinterpret_cast<f32x4*>(f) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(f + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + o) = pack_bf16(v);
+  }
+}
+__device__ __forceinline__ void store1(void* p, int64_t o, int dtype, float v) {
+  if (dtype == 0)
+    static_cast<float*>(p)[o] = v;
+  else
+    static_cast<uint16_t*>(p)[o] = bf16_bits(v);
 }
 
 }  // namespace w4q

@@ -12,75 +12,112 @@
 // matrix cores (nt_gemm.hpp; both operands lie along k already) whose epilogue works on the fp32
 // sums.
 //
-// Backward: both products run along an axis their operands do not lie along, so one pass over each
-// operand writes it transposed (2 B read, 2 B written per value, against 2 d flop of product).  dW
-// and dbias are fp32 results, so dz may not be rounded to bf16: with an activation (or fp32 dy)
-// dz is held as two fp16 parts, 22 bits, and dW = lo x + hi x.  A bf16 value has 8 bits, so x
-// and W are exact in fp16 once a power of two brings their largest value to 2^14 (values below 2^-32
-// of the largest lose bits, an absolute error of 2^-40 of it); the exponents come from one maximum
-// over each tensor and are taken back in the epilogue.  dx is a bf16 result and takes the hi part
-// alone (11 bits, an eighth of the output's own rounding).  Without an activation dz = dy is bf16
-// already: one exact bf16 product each, no scaling.
+// Backward: the products read their operands across their rows where they lie so (dx: W; dW: dz and
+// x), so nothing is transposed in memory.  dW and dbias are fp32 results, so dz may not be rounded
+// to bf16: with an activation (or fp32 dy) dz is held as two fp16 parts, 22 bits, and dW = lo x +
+// hi x.  A bf16 value has 8 bits, so x and W are exact in fp16 once a power of two brings their
+// largest value to 2^14 (values below 2^-32 of the largest lose bits, an absolute error of 2^-40 of
+// it); the exponents come from one maximum over each tensor and are taken back in the epilogue.
+// dx is a bf16 result and takes the hi part alone (11 bits, an eighth of the output's own rounding).
+// Without an activation dz = dy is bf16 already: one exact bf16 product each, no scaling, and x, W
+// and (unless its rows need padding) dy are read as they are.
 #include "epilogue.hpp"
 #include "nt_gemm.hpp"
 
 namespace w4q {
 namespace {
 
-constexpr int kAmaxBlocks = 256;  // partial maxima of one tensor
+constexpr int kAmaxBlocks = 1024; // partial maxima of one tensor
 constexpr float kDactMax = 1.13f; // |act'| <= 1.1290 (gelu), 1.0999 (silu), 1 (relu, none)
 
 // ------------------------------------------------------------------------------ epilogues
 struct EpiLinear {
+  static constexpr bool kMirror = false;
+  struct Pre {
+    u32x4 r0, r1;
+  };
   W4Epilogue ep;
   uint16_t* z;  // bf16 [M][N] or null
   void* y;
   int y_dtype;
+  int vec;      // 8 columns of a row may be moved in 16-byte pieces
 
-  __device__ __forceinline__ void operator()(const NtArgs& g, int, int row0, int col0, bool, const f32x16& acc,
-                                             int lane) const {
-    const int col = col0 + (lane & 31);
-    if (col >= g.N) return;
-    const float bv = ep.bias != nullptr ? ep.bias[col] : 0.0f;
+  __device__ __forceinline__ Pre load(const NtArgs& g, int, int row, int col) const {
+    Pre p = {};
+    if (ep.res != nullptr && vec && row < g.M && col < g.N) load8(ep.res, static_cast<int64_t>(row) * g.N + col, y_dtype, p.r0, p.r1);
+    return p;
+  }
+  __device__ __forceinline__ void store(const NtArgs& g, int, int row, int col, float (&v)[8], const Pre& p) const {
+    if (row >= g.M || col >= g.N) return;
+    const int64_t o = static_cast<int64_t>(row) * g.N + col;
+    const int left = g.N - col;
+    if (ep.bias != nullptr) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int row = row0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-      if (row >= g.M) continue;
-      const int64_t o = static_cast<int64_t>(row) * g.N + col;
-      const float zv = acc[r] + bv;
-      if (z != nullptr) z[o] = bf16_bits(zv);
-      const float v = finish_output(ep, zv, o, y_dtype);
-      if (y_dtype == 0)
-        static_cast<float*>(y)[o] = v;
-      else
-        static_cast<uint16_t*>(y)[o] = bf16_bits(v);
+      for (int e = 0; e < 8; ++e) v[e] += ep.bias[e < left ? col + e : col];
     }
+    if (z != nullptr) {
+      if (vec) {
+        store8(z, o, 1, v);
+      } else {
+        for (int e = 0; e < 8; ++e)
+          if (e < left) z[o + e] = bf16_bits(v[e]);
+      }
+    }
+    float r[8];
+    unpack8(p.r0, p.r1, y_dtype, r);
+    if (ep.res != nullptr && !vec)
+      for (int e = 0; e < 8; ++e)
+        if (e < left)
+          r[e] = y_dtype == 0 ? static_cast<const float*>(ep.res)[o + e] : bf16_val(static_cast<const uint16_t*>(ep.res)[o + e]);
+    // one branch on the activation for all eight values
+    switch (ep.act) {
+      case W4Q_ACT_RELU: act8<W4Q_ACT_RELU>(v); break;
+      case W4Q_ACT_GELU: act8<W4Q_ACT_GELU>(v); break;
+      case W4Q_ACT_SILU: act8<W4Q_ACT_SILU>(v); break;
+      default: break;
+    }
+    if (ep.res != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += r[e];
+    }
+    if (vec) {
+      store8(y, o, y_dtype, v);
+    } else {
+      for (int e = 0; e < 8; ++e)
+        if (e < left) store1(y, o + e, y_dtype, v[e]);
+    }
+  }
+  template <int kAct>
+  static __device__ __forceinline__ void act8(float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = act_fwd(v[e], kAct);
   }
 };
 
-// a gradient product: the operands' powers of two taken back (each on its own, so that no
-// intermediate leaves fp32's range), stored as fp32 or bf16
+// a gradient product: the operands' powers of two taken back, stored as fp32 or bf16
 struct EpiGrad {
+  static constexpr bool kMirror = false;
+  struct Pre {
+    int e;
+  };
   const int* e0;  // exponents of the operands' scales (device), or null
   const int* e1;
   void* out;
-  int out_dtype;
+  int out_dtype, vec;
 
-  __device__ __forceinline__ void operator()(const NtArgs& g, int, int row0, int col0, bool, const f32x16& acc,
-                                             int lane) const {
-    const int col = col0 + (lane & 31);
-    if (col >= g.N) return;
-    const int e = e0 != nullptr ? -(*e0 + *e1) : 0;
+  __device__ __forceinline__ Pre load(const NtArgs&, int, int, int) const {
+    return Pre{e0 != nullptr ? -(*e0 + *e1) : 0};
+  }
+  __device__ __forceinline__ void store(const NtArgs& g, int, int row, int col, float (&v)[8], const Pre& p) const {
+    if (row >= g.M || col >= g.N) return;
+    const int64_t o = static_cast<int64_t>(row) * g.N + col;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int row = row0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-      if (row >= g.M) continue;
-      const int64_t o = static_cast<int64_t>(row) * g.N + col;
-      const float v = __builtin_ldexpf(acc[r], e);
-      if (out_dtype == 0)
-        static_cast<float*>(out)[o] = v;
-      else
-        static_cast<uint16_t*>(out)[o] = bf16_bits(v);
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], p.e);
+    if (vec) {
+      store8(out, o, out_dtype, v);
+    } else {
+      for (int e = 0; e < 8; ++e)
+        if (col + e < g.N) store1(out, o + e, out_dtype, v[e]);
     }
   }
 };
@@ -96,6 +133,7 @@ struct AmaxArgs {
 __global__ __launch_bounds__(256) void amax_kernel(const AmaxArgs a, float* __restrict__ parts) {
   const int t = blockIdx.y;
   const int64_t n = a.n[t];
+  if (n == 0) return;  // not wanted
   float best = 0.0f;
   auto take = [&](float v) {
     v = __builtin_fabsf(v);
@@ -105,6 +143,7 @@ __global__ __launch_bounds__(256) void amax_kernel(const AmaxArgs a, float* __re
   const int64_t step = static_cast<int64_t>(kAmaxBlocks) * 256;
   if (a.f32[t]) {
     const float* p = static_cast<const float*>(a.p[t]);
+#pragma unroll 4
     for (int64_t i = tid; i < n / 4; i += step) {
       const f32x4 v = reinterpret_cast<const f32x4*>(p)[i];
 #pragma unroll
@@ -113,6 +152,7 @@ __global__ __launch_bounds__(256) void amax_kernel(const AmaxArgs a, float* __re
     if (tid < n % 4) take(p[n / 4 * 4 + tid]);
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(a.p[t]);
+#pragma unroll 4
     for (int64_t i = tid; i < n / 8; i += step) {
       const u32x4 v = reinterpret_cast<const u32x4*>(p)[i];
 #pragma unroll
@@ -135,141 +175,150 @@ __global__ __launch_bounds__(256) void amax_kernel(const AmaxArgs a, float* __re
 }
 
 // The exponent e of a tensor's scale from its partial maxima (all 256 threads of the workgroup):
-// bound * amax * 2^e in (2^13, 2^15].  e = 0 for a tensor of zeros.
-__device__ __forceinline__ int scale_exp(const float* __restrict__ parts, float bound) {
-  __shared__ float red[256];
-  red[threadIdx.x] = parts[threadIdx.x];
-  __syncthreads();
+// amax * 2^e in [2^13, 2^14), so kDactMax * amax * 2^e < 2^15.  e = 0 for a tensor of zeros.
+__device__ __forceinline__ int scale_exp(const float* __restrict__ parts) {
+  __shared__ float red[4];
+  float m = 0.0f;
 #pragma unroll
-  for (int o = 128; o >= 1; o >>= 1) {
-    if (static_cast<int>(threadIdx.x) < o) red[threadIdx.x] = __builtin_fmaxf(red[threadIdx.x], red[threadIdx.x + o]);
-    __syncthreads();
-  }
-  const float m = red[0];
+  for (int i = 0; i < kAmaxBlocks / 256; ++i) m = __builtin_fmaxf(m, parts[threadIdx.x + 256 * i]);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
   __syncthreads();
   if (m == 0.0f) return 0;
   int e;
   (void)__builtin_frexpf(m, &e);  // m = f 2^e, f in [0.5, 1)
-  return 14 - e;                  // m 2^(14 - e) in [2^13, 2^14); times 1.13 below 2^15
-}
-static_assert(kAmaxBlocks == 256, "one partial per thread");
-
-__device__ __forceinline__ uint16_t f16_scaled(float v, int e) { return f32_to_f16_bits(__builtin_ldexpf(v, e)); }
-
-// src [rows][cols] bf16 -> dst [cols][rp], rows' ends up to rp (rows rounded up to 32) zero; as bf16, or
-// as fp16 times the power of two of the tensor's maximum (parts != null), whose exponent goes to
-// *exp_out.  64x64 tiles through LDS.
-__device__ __forceinline__ void transpose_tile(const uint16_t* __restrict__ src, int64_t rows, int64_t cols, int64_t rp,
-                                               uint16_t* __restrict__ dst, const float* __restrict__ parts,
-                                               int* __restrict__ exp_out, int64_t bx, int64_t by) {
-  __shared__ uint16_t tile[64][66];
-  int e = 0;
-  if (parts != nullptr) {
-    e = scale_exp(parts, 1.0f);
-    if (bx == 0 && by == 0 && threadIdx.x == 0) *exp_out = e;
-  }
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  const int64_t r0 = by * 64, c0 = bx * 64;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int64_t row = r0 + ty + 4 * i, col = c0 + tx;
-    uint16_t v = 0;
-    if (row < rows && col < cols) {
-      v = src[row * cols + col];
-      if (parts != nullptr) v = f16_scaled(bf16_val(v), e);
-    }
-    tile[ty + 4 * i][tx] = v;
-  }
-  __syncthreads();
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int64_t col = c0 + ty + 4 * i, row = r0 + tx;
-    if (col < cols && row < rp) dst[col * rp + row] = tile[tx][ty + 4 * i];
-  }
+  return 14 - e;
 }
 
-struct TransposeArgs {
-  const uint16_t* src;
-  uint16_t* dst;
-  int64_t rows, cols, rp;
-  const float* parts;
-  int* exp_out;
-  int64_t tiles_x;
+// x and W as fp16 times the power of two of their maxima (exact: 8 significant bits), whose
+// exponents go to exps[1] and exps[2].  blockIdx.y: which.  HBM bound: 4 B per value.
+struct ConvertArgs {
+  const uint16_t* src[2];
+  uint16_t* dst[2];
+  int64_t n8[2];  // eights of values; 0: not wanted
 };
-// x and W in one launch: workgroups below `first` take x's tiles, the others W's
-__global__ __launch_bounds__(256) void transpose_kernel(const TransposeArgs a, const TransposeArgs b, int64_t first) {
-  const int64_t t = blockIdx.x;
-  if (t < first)
-    transpose_tile(a.src, a.rows, a.cols, a.rp, a.dst, a.parts, a.exp_out, t % a.tiles_x, t / a.tiles_x);
-  else
-    transpose_tile(b.src, b.rows, b.cols, b.rp, b.dst, b.parts, b.exp_out, (t - first) % b.tiles_x,
-                   (t - first) / b.tiles_x);
+__global__ __launch_bounds__(256) void convert_kernel(const ConvertArgs a, const float* __restrict__ parts, int* __restrict__ exps) {
+  const int t = blockIdx.y;
+  if (a.n8[t] == 0) return;
+  const int e = scale_exp(parts + (t + 1) * kAmaxBlocks);
+  if (blockIdx.x == 0 && threadIdx.x == 0) exps[t + 1] = e;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+#pragma unroll 2
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < a.n8[t]; i += step) {
+    const u32x4 v = reinterpret_cast<const u32x4*>(a.src[t])[i];
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = f32_to_f16_bits(__builtin_ldexpf(bf16_lo(v[j]), e)) |
+             (static_cast<uint32_t>(f32_to_f16_bits(__builtin_ldexpf(bf16_hi(v[j]), e))) << 16);
+    reinterpret_cast<u32x4*>(a.dst[t])[i] = o;
+  }
 }
 
-// dz = dy act'(z) for 64 x 64 values: hi part along the features (D, for dx) and hi and lo parts along
-// the tokens (T, for dW), the ends up to the next multiple of 32 zero; and the column sums of the tile
-// (fp32, 64 terms) for dbias.  kSplit: fp16 parts of dz 2^e; otherwise (no activation, bf16 dy) dz = dy
-// itself in bf16.
+// dz = dy act'(z), rows padded to np values with zeros: as two fp16 parts of dz 2^e (kSplit), or (no
+// activation, bf16 dy) dy itself; and column sums over the workgroup's 64 rows for dbias.  A thread has
+// 8 columns of a row, a workgroup 256 columns x 64 rows, 8 rows at a time.  HBM bound: dy and z read,
+// 4 (2) B written per value.
+constexpr int kDzRows = 64;
 struct DzArgs {
   const void* dy;
   int dy_f32;
   const uint16_t* z;
-  int act;
-  int64_t m, n, np, mp;
-  uint16_t *d, *th, *tl;  // d, th may be null
-  float* bsum;            // [ceil(m / 64)][n] or null
+  int act, vec;
+  int64_t m, n, np;
+  uint16_t *hi, *lo;  // null: not wanted (the sums alone)
+  float* bsum;        // [ceil(m / 64)][n] or null
   const float* parts;
   int* exp_out;
 };
+template <int kAct>
+__device__ __forceinline__ void dact8(float (&v)[8], const float (&z)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= act_grad(z[j], kAct);
+}
 template <bool kSplit>
 __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
-  __shared__ uint32_t tile[64][65];
-  __shared__ float cs[4][64];
+  __shared__ float cs[8][257];
   int e = 0;
   if constexpr (kSplit) {
-    e = scale_exp(a.parts, kDactMax);
+    e = scale_exp(a.parts);
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.exp_out = e;
   }
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
-  float sum = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int64_t row = r0 + ty + 4 * i, col = c0 + tx;
-    uint32_t packed = 0;
-    if (row < a.m && col < a.n) {
-      const int64_t o = row * a.n + col;
-      float v = a.dy_f32 ? static_cast<const float*>(a.dy)[o] : bf16_val(static_cast<const uint16_t*>(a.dy)[o]);
-      if (a.act != W4Q_ACT_NONE) v *= act_grad(bf16_val(a.z[o]), a.act);
-      sum += v;
-      if constexpr (kSplit) {
-        const float s = __builtin_ldexpf(v, e);
-        const _Float16 hi = static_cast<_Float16>(s);
-        const float rest = s - static_cast<float>(hi);
-        // an infinite dz stays infinite (its rest is NaN)
-        const uint16_t lo = rest == rest ? f32_to_f16_bits(rest) : 0;
-        packed = __builtin_bit_cast(uint16_t, hi) | (static_cast<uint32_t>(lo) << 16);
-      } else {
-        packed = static_cast<const uint16_t*>(a.dy)[o];
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + 8 * (threadIdx.x & 31);
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kDzRows + (threadIdx.x >> 5);
+  float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+  for (int i = 0; i < kDzRows / 8; ++i) {
+    const int64_t row = r0 + 8 * i;
+    if (row >= a.m || col >= a.np) continue;
+    const int64_t o = row * a.n + col;
+    float v[8], zv[8];
+    u32x4 raw = {0, 0, 0, 0};  // dy as it lies (bf16)
+    if (a.vec) {
+      u32x4 d0 = {0, 0, 0, 0}, d1 = {0, 0, 0, 0}, z0 = {0, 0, 0, 0};
+      if (col < a.n) {  // n is a multiple of 8
+        load8(a.dy, o, a.dy_f32 ? 0 : 1, d0, d1);
+        if (a.act != W4Q_ACT_NONE) z0 = *reinterpret_cast<const u32x4*>(a.z + o);
+      }
+      unpack8(d0, d1, a.dy_f32 ? 0 : 1, v);
+      unpack8(z0, z0, 1, zv);
+      raw = d0;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = col + j < a.n;
+        uint16_t bits = 0;
+        if (in && !a.dy_f32) bits = static_cast<const uint16_t*>(a.dy)[o + j];
+        v[j] = !in ? 0.0f : a.dy_f32 ? static_cast<const float*>(a.dy)[o + j] : bf16_val(bits);
+        zv[j] = in && a.act != W4Q_ACT_NONE ? bf16_val(a.z[o + j]) : 0.0f;
+        raw[j >> 1] |= static_cast<uint32_t>(bits) << (16 * (j & 1));
       }
     }
-    tile[ty + 4 * i][tx] = packed;
-    if (a.d != nullptr && row < a.m && col < a.np) a.d[row * a.np + col] = static_cast<uint16_t>(packed);
-  }
-  if (a.bsum != nullptr) cs[ty][tx] = sum;
-  __syncthreads();
-  if (a.bsum != nullptr && ty == 0 && c0 + tx < a.n)
-    a.bsum[blockIdx.y * a.n + c0 + tx] = (cs[0][tx] + cs[1][tx]) + (cs[2][tx] + cs[3][tx]);
-  if (a.th == nullptr) return;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int64_t col = c0 + ty + 4 * i, row = r0 + tx;
-    if (col < a.n && row < a.mp) {
-      const uint32_t packed = tile[tx][ty + 4 * i];
-      a.th[col * a.mp + row] = static_cast<uint16_t>(packed);
-      if constexpr (kSplit) a.tl[col * a.mp + row] = static_cast<uint16_t>(packed >> 16);
+    switch (a.act) {  // (padding columns: 0 times a finite slope)
+      case W4Q_ACT_RELU: dact8<W4Q_ACT_RELU>(v, zv); break;
+      case W4Q_ACT_GELU: dact8<W4Q_ACT_GELU>(v, zv); break;
+      case W4Q_ACT_SILU: dact8<W4Q_ACT_SILU>(v, zv); break;
+      default: break;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    if (a.hi == nullptr) continue;
+    const int64_t at = row * a.np + col;
+    if constexpr (kSplit) {
+      u32x4 h, l;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t hb[2], lb[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float s = __builtin_ldexpf(v[2 * j + q], e);
+          const _Float16 hi = static_cast<_Float16>(s);
+          const float rest = s - static_cast<float>(hi);
+          hb[q] = __builtin_bit_cast(uint16_t, hi);
+          lb[q] = rest == rest ? f32_to_f16_bits(rest) : 0;  // an infinite dz stays infinite (its rest is NaN)
+        }
+        h[j] = hb[0] | (hb[1] << 16);
+        l[j] = lb[0] | (lb[1] << 16);
+      }
+      *reinterpret_cast<u32x4*>(a.hi + at) = h;
+      if (a.lo != nullptr) *reinterpret_cast<u32x4*>(a.lo + at) = l;
+    } else {
+      *reinterpret_cast<u32x4*>(a.hi + at) = raw;
     }
   }
+  if (a.bsum == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cs[threadIdx.x >> 5][8 * (threadIdx.x & 31) + j] = sum[j];
+  __syncthreads();
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= a.n) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s += cs[j][threadIdx.x];
+  a.bsum[blockIdx.y * a.n + c] = s;
 }
 
 // dbias: the tiles' column sums added in row order, in fp64 (one rounding at the end)
@@ -278,17 +327,18 @@ __global__ __launch_bounds__(256) void bias_kernel(const float* __restrict__ bsu
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (col >= n) return;
   double s = 0.0;
+#pragma unroll 8
   for (int64_t t = 0; t < tiles; ++t) s += static_cast<double>(bsum[t * n + col]);
   db[col] = static_cast<float>(s);
 }
 
 // ------------------------------------------------------------------------------ products
-template <int PA, bool F16>
-using Big = NtCfg<256, 256, 128, 64, PA, 1, F16, PA == 1 ? 4 : 3>;
-template <int PA, bool F16>
-using Mid = NtCfg<128, 128, 64, 64, PA, 1, F16, PA == 1 ? 4 : 3>;
-template <int PA, bool F16>
-using Small = NtCfg<64, 64, 32, 32, PA, 1, F16, 4>;
+template <int PA, bool F16, bool AT, bool BT>
+using Big = NtCfg<256, 256, 128, 64, PA, 1, F16, AT, BT, PA == 1 ? 4 : 3>;
+template <int PA, bool F16, bool AT, bool BT>
+using Mid = NtCfg<128, 128, 64, 64, PA, 1, F16, AT, BT, PA == 1 ? 4 : 3>;
+template <int PA, bool F16, bool AT, bool BT>
+using Small = NtCfg<64, 64, 32, 32, PA, 1, F16, AT, BT, 4>;
 
 struct LinPlan {
   int kind;  // 0 Big, 1 Mid, 2 Small
@@ -316,32 +366,32 @@ void fit_plan(LinPlan& r, size_t ws_bytes) {
   r.p.ws = 0;
 }
 
-template <int PA, bool F16, class Epi>
+template <int PA, bool F16, bool AT, bool BT, class Epi>
 int lin_product(const NtArgs& g, const LinPlan& r, const Epi& e, void* ws, hipStream_t s) {
-  if (r.kind == 0) return nt_launch<Big<PA, F16>, Epi>(g, r.p, 0, e, ws, s);
-  if (r.kind == 1) return nt_launch<Mid<PA, F16>, Epi>(g, r.p, 0, e, ws, s);
-  return nt_launch<Small<PA, F16>, Epi>(g, r.p, 0, e, ws, s);
+  if (r.kind == 0) return nt_launch<Big<PA, F16, AT, BT>, Epi>(g, r.p, 0, e, ws, s);
+  if (r.kind == 1) return nt_launch<Mid<PA, F16, AT, BT>, Epi>(g, r.p, 0, e, ws, s);
+  return nt_launch<Small<PA, F16, AT, BT>, Epi>(g, r.p, 0, e, ws, s);
 }
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+inline bool at16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }  // (null too)
 inline int64_t up32(int64_t v) { return (v + 31) / 32 * 32; }
 
 struct BwdLayout {
   bool split;        // dz in two fp16 parts
-  bool direct;       // dx reads dy as it lies
-  int64_t np, mp, mt;
+  bool direct;       // the products read dy as it lies
+  int64_t np, mt;
   LinPlan px, pw;
-  size_t parts, exps, d, th, tl, xt, wt, bsum, part, total;
+  size_t parts, exps, hi, lo, x16, w16, bsum, part, total;
 };
 BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   BwdLayout l;
   l.split = act != W4Q_ACT_NONE || dy_f32 != 0;
   l.np = up32(n);
-  l.mp = up32(m);
-  l.mt = (m + 63) / 64;
+  l.mt = (m + kDzRows - 1) / kDzRows;
   l.direct = !l.split && l.np == n;
   l.px = lin_plan(m, k, l.np);
-  l.pw = lin_plan(n, k, l.mp);
+  l.pw = lin_plan(n, k, m);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -350,11 +400,10 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   };
   l.parts = take(l.split ? 3 * kAmaxBlocks * sizeof(float) : 0);
   l.exps = take(l.split ? 3 * sizeof(int) : 0);
-  l.d = take(l.direct ? 0 : size_t(2) * m * l.np);
-  l.th = take(size_t(2) * n * l.mp);
-  l.tl = take(l.split ? size_t(2) * n * l.mp : 0);
-  l.xt = take(size_t(2) * k * l.mp);
-  l.wt = take(size_t(2) * k * l.np);
+  l.hi = take(l.direct ? 0 : size_t(2) * m * l.np);
+  l.lo = take(l.split ? size_t(2) * m * l.np : 0);
+  l.x16 = take(l.split ? size_t(2) * m * k : 0);
+  l.w16 = take(l.split ? size_t(2) * n * k : 0);
   l.bsum = take(sizeof(float) * l.mt * n);
   const size_t most = l.px.p.ws > l.pw.p.ws ? l.px.p.ws : l.pw.p.ws;
   l.part = take(most);
@@ -375,10 +424,9 @@ using namespace w4q;
 
 bool w4q_linear_fits(int64_t m, int64_t d_out, int64_t d_in, bool backward) {
   if (!backward) return fits(m, d_out, d_in);
-  // one workgroup per 64x64 tile in the passes over the operands
-  if ((m + 63) / 64 > 65535 || (d_out + 63) / 64 > 0x7FFFFFFF || d_in > (1 << 21)) return false;
-  if (((d_in + 63) / 64) * ((m + 63) / 64 + (d_out + 63) / 64 + 2) > 0x7FFFFFFF) return false;
-  return fits(m, d_in, up32(d_out)) && fits(d_out, d_in, up32(m));
+  // one workgroup per 64 rows in the pass over dz; 32 rows of an operand within 32-bit buffer offsets
+  if ((m + kDzRows - 1) / kDzRows > 65535 || d_in > (1 << 21)) return false;
+  return fits(m, d_in, up32(d_out)) && lin_plan(d_out, d_in, m).p.total <= 0x3FFFFFFF;
 }
 
 size_t w4q_linear_fwd_workspace(int64_t m, int64_t d_out, int64_t d_in) { return lin_plan(m, d_out, d_in).p.ws; }
@@ -397,8 +445,9 @@ int w4q_launch_linear_fwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   g.M = static_cast<int>(m);
   g.N = static_cast<int>(d_out);
   g.K = g.lda = g.ldb = static_cast<int>(d_in);
-  const EpiLinear e = {{bias, res, act}, z, y, y_dtype};
-  return lin_product<1, false>(g, p, e, ws, s);
+  const bool vec = d_out % 8 == 0 && at16(y) && at16(z) && at16(res);
+  const EpiLinear e = {{bias, res, act}, z, y, y_dtype, vec ? 1 : 0};
+  return lin_product<1, false, false, false>(g, p, e, ws, s);
 }
 
 int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,
@@ -409,60 +458,60 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   auto u16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(base + off); };
   float* parts = l.split ? reinterpret_cast<float*>(base + l.parts) : nullptr;
   int* exps = l.split ? reinterpret_cast<int*>(base + l.exps) : nullptr;  // dy, x, W
+  float* bsum = db != nullptr ? reinterpret_cast<float*>(base + l.bsum) : nullptr;
   void* part = base + l.part;
+  const bool products = dx != nullptr || dw != nullptr;
   int rc = W4Q_OK;
-  if (l.split) {
-    AmaxArgs a = {{dy, x, w_hat}, {m * d_out, m * d_in, d_out * d_in}, {dy_f32, 0, 0}};
+  if (l.split && products) {
+    const AmaxArgs a = {{dy, x, w_hat}, {m * d_out, dw != nullptr ? m * d_in : 0, dx != nullptr ? d_out * d_in : 0}, {dy_f32, 0, 0}};
     hipLaunchKernelGGL(amax_kernel, dim3(kAmaxBlocks, 3), dim3(256), 0, s, a, parts);
     if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
+    const ConvertArgs c = {{x, w_hat}, {u16(l.x16), u16(l.w16)}, {dw != nullptr ? m * d_in / 8 : 0, dx != nullptr ? d_out * d_in / 8 : 0}};
+    const int64_t most = (c.n8[0] > c.n8[1] ? c.n8[0] : c.n8[1]) / 512 + 1;
+    hipLaunchKernelGGL(convert_kernel, dim3(static_cast<unsigned>(most < 2048 ? most : 2048), 2), dim3(256), 0, s, c, parts, exps);
+    if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
   }
-  const bool need_d = dx != nullptr && !l.direct;
-  if (need_d || dw != nullptr || db != nullptr) {
-    DzArgs a = {dy, dy_f32, z, act, m, d_out, l.np, l.mp, need_d ? u16(l.d) : nullptr, dw != nullptr ? u16(l.th) : nullptr,
-                u16(l.tl), db != nullptr ? reinterpret_cast<float*>(base + l.bsum) : nullptr, parts, exps};
-    const dim3 grid(static_cast<unsigned>((l.np + 63) / 64), static_cast<unsigned>(l.mt));
-    if (l.split)
+  const bool need = products && !l.direct;
+  if (need || db != nullptr) {
+    const bool vec = d_out % 8 == 0 && at16(z);
+    const DzArgs a = {dy, dy_f32, z, act, vec ? 1 : 0, m, d_out, l.np, need ? u16(l.hi) : nullptr,
+                      l.split && dw != nullptr ? u16(l.lo) : nullptr, bsum, parts, exps};
+    const dim3 grid(static_cast<unsigned>((l.np + 255) / 256), static_cast<unsigned>(l.mt));
+    if (l.split && need)
       hipLaunchKernelGGL(dz_kernel<true>, grid, dim3(256), 0, s, a);
     else
       hipLaunchKernelGGL(dz_kernel<false>, grid, dim3(256), 0, s, a);
     if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
   }
   if (db != nullptr) {
-    hipLaunchKernelGGL(bias_kernel, dim3(static_cast<unsigned>((d_out + 255) / 256)), dim3(256), 0, s,
-                       reinterpret_cast<const float*>(base + l.bsum), l.mt, d_out, db);
+    hipLaunchKernelGGL(bias_kernel, dim3(static_cast<unsigned>((d_out + 255) / 256)), dim3(256), 0, s, bsum, l.mt, d_out, db);
     if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
   }
-  if (dx == nullptr && dw == nullptr) return rc;
-  const int64_t tk = (d_in + 63) / 64;
-  const TransposeArgs tx = {x, u16(l.xt), m, d_in, l.mp, l.split ? parts + kAmaxBlocks : nullptr,
-                            l.split ? exps + 1 : nullptr, tk};
-  const TransposeArgs tw = {w_hat, u16(l.wt), d_out, d_in, l.np, l.split ? parts + 2 * kAmaxBlocks : nullptr,
-                            l.split ? exps + 2 : nullptr, tk};
-  const int64_t nx = dw != nullptr ? tk * l.mt : 0;
-  const int64_t nw = dx != nullptr ? tk * ((d_out + 63) / 64) : 0;
-  hipLaunchKernelGGL(transpose_kernel, dim3(static_cast<unsigned>(nx + nw)), dim3(256), 0, s, tx, tw, nx);
-  if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
-  if (dx != nullptr) {  // dx [m][d_in] = dz W
+  const uint16_t* hi = l.direct ? static_cast<const uint16_t*>(dy) : u16(l.hi);
+  const bool vec = at16(dx) && at16(dw);  // (rows of d_in, a multiple of 32, values)
+  if (dx != nullptr) {  // dx [m][d_in] = dz W: dz along n, W across
     NtArgs g = {};
-    g.a[0] = l.direct ? static_cast<const uint16_t*>(dy) : u16(l.d);
-    g.b[0] = u16(l.wt);
+    g.a[0] = hi;
+    g.b[0] = l.split ? u16(l.w16) : w_hat;
     g.M = static_cast<int>(m);
-    g.N = static_cast<int>(d_in);
-    g.K = g.lda = g.ldb = static_cast<int>(l.np);
-    const EpiGrad e = {exps, exps + 2, dx, 1};
-    rc = l.split ? lin_product<1, true>(g, l.px, e, part, s) : lin_product<1, false>(g, l.px, EpiGrad{nullptr, nullptr, dx, 1}, part, s);
+    g.N = g.ldb = static_cast<int>(d_in);
+    g.K = g.lda = static_cast<int>(l.np);
+    g.kb = static_cast<int>(d_out);
+    const EpiGrad e = {exps, l.split ? exps + 2 : nullptr, dx, 1, vec ? 1 : 0};
+    rc = l.split ? lin_product<1, true, false, true>(g, l.px, e, part, s) : lin_product<1, false, false, true>(g, l.px, e, part, s);
     if (rc != W4Q_OK) return rc;
   }
-  if (dw != nullptr) {  // dW [d_out][d_in] = dz^T x
+  if (dw != nullptr) {  // dW [d_out][d_in] = dz^T x: both across
     NtArgs g = {};
-    g.a[0] = u16(l.th);
-    g.a[1] = u16(l.tl);
-    g.b[0] = u16(l.xt);
+    g.a[0] = hi;
+    g.a[1] = u16(l.lo);
+    g.b[0] = l.split ? u16(l.x16) : x;
     g.M = static_cast<int>(d_out);
-    g.N = static_cast<int>(d_in);
-    g.K = g.lda = g.ldb = static_cast<int>(l.mp);
-    const EpiGrad e = {exps, exps + 1, dw, 0};
-    rc = l.split ? lin_product<2, true>(g, l.pw, e, part, s) : lin_product<1, false>(g, l.pw, EpiGrad{nullptr, nullptr, dw, 0}, part, s);
+    g.N = g.ldb = static_cast<int>(d_in);
+    g.lda = static_cast<int>(l.np);
+    g.K = g.ka = g.kb = static_cast<int>(m);
+    const EpiGrad e = {exps, l.split ? exps + 1 : nullptr, dw, 0, vec ? 1 : 0};
+    rc = l.split ? lin_product<2, true, true, true>(g, l.pw, e, part, s) : lin_product<1, false, true, true>(g, l.pw, e, part, s);
   }
   return rc;
 }

@@ -19,9 +19,11 @@
 // mirrored), B X is whole: n^2 k + n^3 + 2 n^2 k flop, times three products.  Matrix-core bound from
 // n of about 1024 up; below that the chain of dependent launches is what costs.
 //
-// Layouts: the products run along rows of both operands, so X is kept as XN [n][k] (the Gram
-// product) and XT [k][n] (the update); each epilogue writes both.  XN is updated in place (element by
-// element), XT alternates between two buffers (other tiles still read the old one).
+// Layouts: X stays as U lies, [rows][cols] with rows padded to a multiple of 32 values, in two buffers
+// that alternate (other tiles still read the old one).  Where rows > cols the iteration is written
+// for Y = X^T: A = Y^T Y, Y <- a Y + Y B (B is symmetric).  The products read operands along or across
+// their rows, so nothing is transposed in memory.
+#include "epilogue.hpp"
 #include "nt_gemm.hpp"
 
 namespace w4q {
@@ -38,88 +40,117 @@ __device__ __forceinline__ void split16(float v, uint16_t& h, uint16_t& l) {
 }
 
 // ------------------------------------------------------------------------- epilogues
-// alpha * C + beta * acc, split, to the output and (transposed) to the second output
-struct EpiSplit {
-  const uint16_t *ch, *cl;  // C term or null
-  int ldc;
-  int64_t sc;
-  float alpha, beta;
-  uint16_t *oh, *ol;
-  int ldo;
-  int64_t so;
-  uint16_t *th, *tl;  // transposed output [N][ldt]
-  int ldt;
-  int64_t st;
-  int mirror;  // symmetric result: the transposed store only off the diagonal tiles
+__device__ __forceinline__ void split8(const float (&v)[8], u32x4& h, u32x4& l) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint16_t h0, l0, h1, l1;
+    split16(v[2 * i], h0, l0);
+    split16(v[2 * i + 1], h1, l1);
+    h[i] = h0 | (static_cast<uint32_t>(h1) << 16);
+    l[i] = l0 | (static_cast<uint32_t>(l1) << 16);
+  }
+}
+__device__ __forceinline__ void join8(const u32x4& h, const u32x4& l, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = f16_bits_to_f32(static_cast<uint16_t>(h[i])) + f16_bits_to_f32(static_cast<uint16_t>(l[i]));
+    v[2 * i + 1] = f16_bits_to_f32(static_cast<uint16_t>(h[i] >> 16)) + f16_bits_to_f32(static_cast<uint16_t>(l[i] >> 16));
+  }
+}
 
-  __device__ __forceinline__ void operator()(const NtArgs& g, int batch, int row0, int col0, bool diag,
-                                             const f32x16& acc, int lane) const {
-    const int col = col0 + (lane & 31);
-    const bool tr = col < g.N && !(mirror != 0 && diag);
+// a split matrix [rows][ld] per batch, ld a multiple of 32
+struct Split {
+  uint16_t *h, *l;
+  int ld;
+  int64_t stride;
+};
+struct Pair8 {
+  u32x4 h, l;
+};
+__device__ __forceinline__ Pair8 load_pair(const Split& m, int batch, int row, int col) {
+  const int64_t o = batch * m.stride + static_cast<int64_t>(row) * m.ld + col;
+  return Pair8{*reinterpret_cast<const u32x4*>(m.h + o), *reinterpret_cast<const u32x4*>(m.l + o)};
+}
+
+// alpha * C + beta * acc, split, as the output (its rows' padding, where both terms are zero, included);
+// kSym: a symmetric result of which only the tiles on and below the diagonal are computed: the
+// others get the transposed values
+template <bool kSym>
+struct EpiSplit {
+  static constexpr bool kMirror = kSym;
+  using Pre = Pair8;
+  Split c;  // C term; c.h null: none
+  float alpha, beta;
+  Split o;
+
+  __device__ __forceinline__ Pre load(const NtArgs& g, int batch, int row, int col) const {
+    Pre p = {};
+    if (c.h != nullptr && row < g.M && col < c.ld) p = load_pair(c, batch, row, col);
+    return p;
+  }
+  __device__ __forceinline__ void put(int batch, int row, int col, const float (&v)[8]) const {
+    const int64_t at = batch * o.stride + static_cast<int64_t>(row) * o.ld + col;
+    u32x4 h, l;
+    split8(v, h, l);
+    *reinterpret_cast<u32x4*>(o.h + at) = h;
+    *reinterpret_cast<u32x4*>(o.l + at) = l;
+  }
+  __device__ __forceinline__ void store(const NtArgs& g, int batch, int row, int col, float (&v)[8], const Pre& p) const {
+    float t[8];
+    join8(p.h, p.l, t);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int rq = row0 + 8 * q + 4 * (lane >> 5);
-      u16x4 h4, l4;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = rq + e;
-        const bool in = row < g.M && col < ldo;
-        float v = beta * acc[4 * q + e];
-        if (ch != nullptr && in) {
-          const int64_t o = batch * sc + static_cast<int64_t>(row) * ldc + col;
-          v = __builtin_fmaf(alpha, f16_bits_to_f32(ch[o]) + f16_bits_to_f32(cl[o]), v);
-        }
-        uint16_t h, l;
-        split16(v, h, l);
-        h4[e] = h;
-        l4[e] = l;
-        if (in) {
-          const int64_t o = batch * so + static_cast<int64_t>(row) * ldo + col;
-          oh[o] = h;
-          ol[o] = l;
-        }
-      }
-      if (tr && rq < ldt) {  // ldt is a multiple of 32 and rq of 4: all four rows or none
-        const int64_t o = batch * st + static_cast<int64_t>(col) * ldt + rq;
-        *reinterpret_cast<u16x4*>(th + o) = h4;
-        *reinterpret_cast<u16x4*>(tl + o) = l4;
-      }
-    }
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(alpha, t[e], beta * v[e]);
+    if (row < g.M && col < o.ld) put(batch, row, col, v);
+  }
+  __device__ __forceinline__ void store_t(const NtArgs& g, int batch, int col, int row, const float (&v)[8]) const {
+    if (col < g.N && row < o.ld) put(batch, col, row, v);
   }
 };
 
-// the last update: o = (alpha * C + beta * acc) 2^-13, stored as the result or applied to the weights
+// the last update: o = (alpha * X + beta * acc) 2^-13, stored as the result or applied to the weights
 struct EpiLast {
-  const uint16_t *ch, *cl;
-  int ldc;
-  int64_t sc;
+  static constexpr bool kMirror = false;
+  struct Pre {
+    Pair8 x;
+    u32x4 w0, w1;
+  };
+  Split x;
   float alpha, beta;
-  void* out;       // newton_schulz: [M][N] fp32 (dtype 0) or bf16 (1)
+  void* out;      // newton_schulz: [M][N] fp32 (dtype 0) or bf16 (1)
   int out_dtype;
-  float* w;        // muon_step: fp32 [M][N], updated in place (out is null then)
+  float* w;       // muon_step: fp32 [M][N], updated in place (out is null then)
   float lr, scale, wd;
+  int vec;        // 8 columns of a row may be moved in 16-byte pieces
 
-  __device__ __forceinline__ void operator()(const NtArgs& g, int batch, int row0, int col0, bool, const f32x16& acc,
-                                             int lane) const {
-    const int col = col0 + (lane & 31);
-    if (col >= g.N) return;
-    const int64_t base = static_cast<int64_t>(batch) * g.M * g.N;
+  __device__ __forceinline__ Pre load(const NtArgs& g, int batch, int row, int col) const {
+    Pre p = {};
+    if (row < g.M && col < x.ld) p.x = load_pair(x, batch, row, col);
+    if (w != nullptr && vec && row < g.M && col < g.N)
+      load8(w, (static_cast<int64_t>(batch) * g.M + row) * g.N + col, 0, p.w0, p.w1);
+    return p;
+  }
+  __device__ __forceinline__ void store(const NtArgs& g, int batch, int row, int col, float (&v)[8], const Pre& p) const {
+    if (row >= g.M || col >= g.N) return;
+    const int64_t o = (static_cast<int64_t>(batch) * g.M + row) * g.N + col;
+    float t[8], wv[8];
+    join8(p.x.h, p.x.l, t);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int row = row0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-      if (row >= g.M) continue;
-      const int64_t o = batch * sc + static_cast<int64_t>(row) * ldc + col;
-      const float x = f16_bits_to_f32(ch[o]) + f16_bits_to_f32(cl[o]);
-      const float v = __builtin_fmaf(alpha, x, beta * acc[r]) * kSplitInv;
-      const int64_t y = base + static_cast<int64_t>(row) * g.N + col;
-      if (w != nullptr) {
-        const float wv = w[y];
-        w[y] = wv - lr * (scale * v + wd * wv);
-      } else if (out_dtype == 0) {
-        static_cast<float*>(out)[y] = v;
-      } else {
-        static_cast<uint16_t*>(out)[y] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-      }
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(alpha, t[e], beta * v[e]) * kSplitInv;
+    if (w != nullptr) {
+      unpack8(p.w0, p.w1, 0, wv);
+      if (!vec)
+        for (int e = 0; e < 8; ++e)
+          if (col + e < g.N) wv[e] = w[o + e];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = wv[e] - lr * (scale * v[e] + wd * wv[e]);
+    }
+    void* to = w != nullptr ? static_cast<void*>(w) : out;
+    const int dt = w != nullptr ? 0 : out_dtype;
+    if (vec) {
+      store8(to, o, dt, v);
+    } else {
+      for (int e = 0; e < 8; ++e)
+        if (col + e < g.N) store1(to, o + e, dt, v[e]);
     }
   }
 };
@@ -141,95 +172,138 @@ __device__ __forceinline__ float grad_at(const Source& s, int64_t i) {
                       : __builtin_bit_cast(float, static_cast<uint32_t>(static_cast<const uint16_t*>(s.g)[i]) << 16);
 }
 
+// Where a matrix's elements start on a 16-byte boundary (vec), values are taken four at a time.
+__device__ __forceinline__ void grad4(const Source& s, int64_t i, float (&g)[4]) {
+  if (s.dtype == 0) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(s.g) + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) g[e] = v[e];
+  } else {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(s.g) + i);
+    g[0] = bf16_lo(v[0]);
+    g[1] = bf16_hi(v[0]);
+    g[2] = bf16_lo(v[1]);
+    g[3] = bf16_hi(v[1]);
+  }
+}
+
+// sum over a workgroup of 256 in a fixed order (all threads get it)
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double red[4];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
 // sum of the squares of U over one share of a matrix, in fp64 (exact products); with a momentum
 // buffer, m <- mu m + g first and U = g + mu m (nesterov) or m.  HBM bound: one read of g (and of m,
 // with its write).
-__global__ __launch_bounds__(256) void norm_kernel(const Source s, int64_t elems, int parts, double* __restrict__ sums) {
+__global__ __launch_bounds__(256) void norm_kernel(const Source s, int64_t elems, int parts, int vec, double* __restrict__ sums) {
   const int batch = blockIdx.y;
   const int64_t base = static_cast<int64_t>(batch) * elems;
   double acc = 0.0;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < elems; i += static_cast<int64_t>(parts) * 256) {
-    const float g = grad_at(s, base + i);
+  auto one = [&](float g, float& m) {
     float u = g;
     if (s.m != nullptr) {
-      const float m = __builtin_fmaf(s.mu, s.m[base + i], g);
-      s.m[base + i] = m;
+      m = __builtin_fmaf(s.mu, m, g);
       u = s.nesterov ? __builtin_fmaf(s.mu, m, g) : m;
     }
     acc = __builtin_fma(static_cast<double>(u), static_cast<double>(u), acc);
-  }
-  __shared__ double red[256];
-  red[threadIdx.x] = acc;
-  __syncthreads();
+  };
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<int64_t>(parts) * 256;
+  if (vec) {
+#pragma unroll 4
+    for (int64_t i = t; i < elems / 4; i += step) {
+      float g[4], m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      grad4(s, base + 4 * i, g);
+      if (s.m != nullptr) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(s.m + base + 4 * i);
 #pragma unroll
-  for (int o = 128; o >= 1; o >>= 1) {
-    if (static_cast<int>(threadIdx.x) < o) red[threadIdx.x] += red[threadIdx.x + o];
-    __syncthreads();
+        for (int e = 0; e < 4; ++e) m[e] = v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) one(g[e], m[e]);
+      if (s.m != nullptr) *reinterpret_cast<f32x4*>(s.m + base + 4 * i) = f32x4{m[0], m[1], m[2], m[3]};
+    }
+  } else {
+    for (int64_t i = t; i < elems; i += step) {
+      float m = s.m != nullptr ? s.m[base + i] : 0.0f;
+      one(grad_at(s, base + i), m);
+      if (s.m != nullptr) s.m[base + i] = m;
+    }
   }
-  if (threadIdx.x == 0) sums[static_cast<int64_t>(batch) * parts + blockIdx.x] = red[0];
+  acc = block_sum(acc);
+  if (threadIdx.x == 0) sums[static_cast<int64_t>(batch) * parts + blockIdx.x] = acc;
 }
 
-// U / (||U|| + eps), split, in both layouts: P [rows][cp] as U lies and Q [cols][rp] transposed, the
-// rows' ends up to the next multiple of 32 zero.  64x64 tiles through LDS.
-__global__ __launch_bounds__(256) void first_split_kernel(const Source s, int rows, int cols, int parts,
-                                                          const double* __restrict__ sums, double eps,
-                                                          uint16_t* __restrict__ ph, uint16_t* __restrict__ pl, int cp,
-                                                          uint16_t* __restrict__ qh, uint16_t* __restrict__ ql, int rp) {
-  __shared__ double red[256];
-  __shared__ uint32_t tile[64][65];
-  const int batch = blockIdx.z;
+// U / (||U|| + eps), split, [rows][ld] with the rows' ends zero; 8 values of a row per thread.  HBM
+// bound: one read of g (and m), 4 bytes written per value.
+__global__ __launch_bounds__(256) void first_split_kernel(const Source s, int64_t rows, int cols, int parts, int vec,
+                                                          const double* __restrict__ sums, double eps, const Split o) {
+  const int batch = blockIdx.y;
   const double* sb = sums + static_cast<int64_t>(batch) * parts;
   double acc = 0.0;
   for (int i = threadIdx.x; i < parts; i += 256) acc += sb[i];
-  red[threadIdx.x] = acc;
-  __syncthreads();
-#pragma unroll
-  for (int o = 128; o >= 1; o >>= 1) {
-    if (static_cast<int>(threadIdx.x) < o) red[threadIdx.x] += red[threadIdx.x + o];
-    __syncthreads();
-  }
-  const double inv = 1.0 / (__builtin_sqrt(red[0]) + eps);
-
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  const double inv = 1.0 / (__builtin_sqrt(block_sum(acc)) + eps);
   const int64_t base = static_cast<int64_t>(batch) * rows * cols;
-  const int64_t pb = static_cast<int64_t>(batch) * rows * cp, qb = static_cast<int64_t>(batch) * cols * rp;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int row = r0 + ty + 4 * i, col = c0 + tx;
-    uint32_t packed = 0;
-    if (row < rows && col < cols) {
-      const int64_t o = base + static_cast<int64_t>(row) * cols + col;
-      const float g = grad_at(s, o);
-      float u = g;
-      if (s.m != nullptr) u = s.nesterov ? __builtin_fmaf(s.mu, s.m[o], g) : s.m[o];
-      const float x = static_cast<float>(static_cast<double>(u) * inv) * kSplitScale;
-      uint16_t h, l;
-      split16(x, h, l);
-      packed = h | (static_cast<uint32_t>(l) << 16);
+  const int per_row = o.ld / 8;
+  const int64_t n8 = rows * per_row;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = i / per_row;
+    const int col = static_cast<int>(i - row * per_row) * 8;
+    const int64_t at = base + row * cols + col;
+    float g[8], m[8], v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = m[e] = 0.0f;
+    if (vec) {  // cols is a multiple of 8: all eight values or none
+      if (col < cols) {
+        float a[4], b[4];
+        grad4(s, at, a);
+        grad4(s, at + 4, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          g[e] = a[e];
+          g[4 + e] = b[e];
+        }
+        if (s.m != nullptr) {
+          const f32x4 c = *reinterpret_cast<const f32x4*>(s.m + at), d = *reinterpret_cast<const f32x4*>(s.m + at + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            m[e] = c[e];
+            m[4 + e] = d[e];
+          }
+        }
+      }
+    } else {
+      for (int e = 0; e < 8; ++e)
+        if (col + e < cols) {
+          g[e] = grad_at(s, at + e);
+          if (s.m != nullptr) m[e] = s.m[at + e];
+        }
     }
-    tile[ty + 4 * i][tx] = packed;
-    if (row < rows && col < cp) {
-      ph[pb + static_cast<int64_t>(row) * cp + col] = static_cast<uint16_t>(packed);
-      pl[pb + static_cast<int64_t>(row) * cp + col] = static_cast<uint16_t>(packed >> 16);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u = s.m == nullptr ? g[e] : s.nesterov ? __builtin_fmaf(s.mu, m[e], g[e]) : m[e];
+      // the padding stays zero even where the norm is not finite
+      v[e] = col + e < cols ? static_cast<float>(static_cast<double>(u) * inv) * kSplitScale : 0.0f;
     }
-  }
-  __syncthreads();
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int col = c0 + ty + 4 * i, row = r0 + tx;
-    if (col < cols && row < rp) {
-      const uint32_t packed = tile[tx][ty + 4 * i];
-      qh[qb + static_cast<int64_t>(col) * rp + row] = static_cast<uint16_t>(packed);
-      ql[qb + static_cast<int64_t>(col) * rp + row] = static_cast<uint16_t>(packed >> 16);
-    }
+    u32x4 h, l;
+    split8(v, h, l);
+    const int64_t to = batch * o.stride + row * o.ld + col;
+    *reinterpret_cast<u32x4*>(o.h + to) = h;
+    *reinterpret_cast<u32x4*>(o.l + to) = l;
   }
 }
 
 // ------------------------------------------------------------------------- the products
-using Big = NtCfg<256, 256, 128, 64, 2, 2, true, 2>;
-using Mid = NtCfg<128, 128, 64, 64, 2, 2, true, 2>;
-using Small = NtCfg<64, 64, 32, 32, 2, 2, true, 3>;
+template <bool AT, bool BT>
+using Big = NtCfg<256, 256, 128, 64, 2, 2, true, AT, BT, 2>;
+template <bool AT, bool BT>
+using Mid = NtCfg<128, 128, 64, 64, 2, 2, true, AT, BT, 2>;
+template <bool AT, bool BT>
+using Small = NtCfg<64, 64, 32, 32, 2, 2, true, AT, BT, 3, true>;
 
 struct NsPlan {
   int kind;  // 0 Big, 1 Mid, 2 Small
@@ -239,64 +313,63 @@ struct NsPlan {
 // Tile size by how many tiles there are: the largest one that still gives most compute units work.
 NsPlan ns_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri) {
   NsPlan r;
-  r.p = nt_plan(batch, M, N, K, tri, Big::BM, Big::BN, kNtCus);
+  r.p = nt_plan(batch, M, N, K, tri, 256, 256, kNtCus);
   r.kind = 0;
   if (batch * r.p.per_batch >= 96) return r;
-  r.p = nt_plan(batch, M, N, K, tri, Mid::BM, Mid::BN, 2 * kNtCus);
+  r.p = nt_plan(batch, M, N, K, tri, 128, 128, 2 * kNtCus);
   r.kind = 1;
   if (batch * r.p.per_batch >= 128) return r;
-  r.p = nt_plan(batch, M, N, K, tri, Small::BM, Small::BN, 3 * kNtCus);
+  r.p = nt_plan(batch, M, N, K, tri, 64, 64, 3 * kNtCus);
   r.kind = 2;
   return r;
 }
 
-template <class Epi>
+template <bool AT, bool BT, class Epi>
 int ns_product(const NtArgs& g, const NsPlan& r, int tri, const Epi& e, void* ws, hipStream_t s) {
-  if (r.kind == 0) return nt_launch<Big, Epi>(g, r.p, tri, e, ws, s);
-  if (r.kind == 1) return nt_launch<Mid, Epi>(g, r.p, tri, e, ws, s);
-  return nt_launch<Small, Epi>(g, r.p, tri, e, ws, s);
+  if (r.kind == 0) return nt_launch<Big<AT, BT>, Epi>(g, r.p, tri, e, ws, s);
+  if (r.kind == 1) return nt_launch<Mid<AT, BT>, Epi>(g, r.p, tri, e, ws, s);
+  return nt_launch<Small<AT, BT>, Epi>(g, r.p, tri, e, ws, s);
 }
 
 struct NsLayout {
-  int64_t n, k, np, kp;
-  NsPlan gram, poly, upd, last;
+  bool wide;            // rows <= cols
+  int64_t n, np, ld;    // the smaller side, padded; X's row length (cols, padded)
+  NsPlan gram, poly, upd;
   int parts;
-  size_t sums, xn, xt, aa, bb, part, total;  // byte offsets (each hi then lo), end
-  size_t xn1, xt1, nn1;                      // bytes of one part
+  size_t sums, x0, x1, aa, bb, part, total;  // byte offsets (each matrix hi then lo), end
+  size_t x_bytes, n_bytes;                   // bytes of one part
 };
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
   NsLayout l;
-  l.n = rows < cols ? rows : cols;
-  l.k = rows < cols ? cols : rows;
+  l.wide = rows <= cols;
+  l.n = l.wide ? rows : cols;
   l.np = (l.n + 31) / 32 * 32;
-  l.kp = (l.k + 31) / 32 * 32;
-  l.gram = ns_plan(batch, l.n, l.n, l.kp, true);
+  l.ld = (cols + 31) / 32 * 32;
+  l.gram = ns_plan(batch, l.n, l.n, l.wide ? l.ld : rows, true);
   l.poly = ns_plan(batch, l.n, l.n, l.np, true);
-  l.upd = ns_plan(batch, l.n, l.k, l.np, false);
-  l.last = rows <= cols ? l.upd : ns_plan(batch, l.k, l.n, l.np, false);
+  l.upd = ns_plan(batch, rows, cols, l.np, false);
   const int64_t parts = (rows * cols + kPerPart - 1) / kPerPart;
   l.parts = static_cast<int>(parts < kPartMax ? parts : kPartMax);
-  l.xn1 = up256(size_t(2) * batch * l.n * l.kp);
-  l.xt1 = up256(size_t(2) * batch * l.k * l.np);
-  l.nn1 = up256(size_t(2) * batch * l.n * l.np);
+  l.x_bytes = up256(size_t(2) * batch * rows * l.ld);
+  l.n_bytes = up256(size_t(2) * batch * l.n * l.np);
   size_t o = 0;
-  l.sums = o;
-  o += up256(sizeof(double) * batch * l.parts);
-  l.xn = o;
-  o += 2 * l.xn1;
-  l.xt = o;
-  o += 4 * l.xt1;  // two of them
-  l.aa = o;
-  o += 2 * l.nn1;
-  l.bb = o;
-  o += 2 * l.nn1;
-  l.part = o;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += up256(bytes);
+    return at;
+  };
+  l.sums = take(sizeof(double) * batch * l.parts);
+  l.x0 = take(2 * l.x_bytes);
+  l.x1 = take(2 * l.x_bytes);
+  l.aa = take(2 * l.n_bytes);
+  l.bb = take(2 * l.n_bytes);
   size_t most = 0;
-  for (const NsPlan* p : {&l.gram, &l.poly, &l.upd, &l.last}) most = p->p.ws > most ? p->p.ws : most;
-  l.total = o + up256(most);
+  for (const NsPlan* p : {&l.gram, &l.poly, &l.upd}) most = p->p.ws > most ? p->p.ws : most;
+  l.part = take(most);
+  l.total = o;
   return l;
 }
 
@@ -308,7 +381,7 @@ using namespace w4q;
 bool w4q_ns_fits(int64_t batch, int64_t rows, int64_t cols) {
   if (batch > 65535 || rows > 131072 || cols > 131072) return false;
   const NsLayout l = ns_layout(batch, rows, cols);
-  for (const NsPlan* p : {&l.gram, &l.poly, &l.upd, &l.last})
+  for (const NsPlan* p : {&l.gram, &l.poly, &l.upd})
     if (p->p.total > 0x3FFFFFFF) return false;
   return true;
 }
@@ -359,95 +432,77 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
   const NsLayout l = ns_layout(batch, rows, cols);
   uint8_t* base = static_cast<uint8_t*>(ws);
   double* sums = reinterpret_cast<double*>(base + l.sums);
-  auto u16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(base + off); };
-  uint16_t *xnh = u16(l.xn), *xnl = u16(l.xn + l.xn1);
-  uint16_t* xth[2] = {u16(l.xt), u16(l.xt + 2 * l.xt1)};
-  uint16_t* xtl[2] = {u16(l.xt + l.xt1), u16(l.xt + 3 * l.xt1)};
-  uint16_t *ah = u16(l.aa), *al = u16(l.aa + l.nn1);
-  uint16_t *bh = u16(l.bb), *bl = u16(l.bb + l.nn1);
+  auto split = [&](size_t off, size_t bytes, int64_t ld, int64_t stride) {
+    return Split{reinterpret_cast<uint16_t*>(base + off), reinterpret_cast<uint16_t*>(base + off + bytes),
+                 static_cast<int>(ld), stride};
+  };
+  Split x[2] = {split(l.x0, l.x_bytes, l.ld, rows * l.ld), split(l.x1, l.x_bytes, l.ld, rows * l.ld)};
+  const Split A = split(l.aa, l.n_bytes, l.np, l.n * l.np), B = split(l.bb, l.n_bytes, l.np, l.n * l.np);
   void* part = base + l.part;
-  const bool wide = rows <= cols;
-  const int n = static_cast<int>(l.n), k = static_cast<int>(l.k), np = static_cast<int>(l.np), kp = static_cast<int>(l.kp);
-  const int64_t sxn = l.n * l.kp, sxt = l.k * l.np, snn = l.n * l.np;
+  const int n = static_cast<int>(l.n), np = static_cast<int>(l.np);
 
+  auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   const Source src = {g, g_dtype, m, mu, nesterov};
+  const bool vec = cols % 8 == 0 && at16(g) && (m == nullptr || at16(m));
   hipLaunchKernelGGL(norm_kernel, dim3(static_cast<unsigned>(l.parts), static_cast<unsigned>(batch)), dim3(256), 0, s, src,
-                     rows * cols, l.parts, sums);
+                     rows * cols, l.parts, vec ? 1 : 0, sums);
   int rc = w4q_launch_status();
   if (rc != W4Q_OK) return rc;
-  const int cp = wide ? kp : np, rp = wide ? np : kp;
-  hipLaunchKernelGGL(first_split_kernel,
-                     dim3(static_cast<unsigned>((cols + 63) / 64), static_cast<unsigned>((rows + 63) / 64),
-                          static_cast<unsigned>(batch)),
-                     dim3(256), 0, s, src, static_cast<int>(rows), static_cast<int>(cols), l.parts, sums, eps,
-                     wide ? xnh : xth[0], wide ? xnl : xtl[0], cp, wide ? xth[0] : xnh, wide ? xtl[0] : xnl, rp);
+  const int64_t blocks = (rows * l.ld / 8 + 255) / 256;
+  hipLaunchKernelGGL(first_split_kernel, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), static_cast<unsigned>(batch)),
+                     dim3(256), 0, s, src, rows, static_cast<int>(cols), l.parts, vec ? 1 : 0, sums, eps, x[0]);
   rc = w4q_launch_status();
+
+  auto operand = [](const Split& m, const uint16_t* (&parts)[2], int64_t& stride, int& ld) {
+    parts[0] = m.h;
+    parts[1] = m.l;
+    stride = m.stride;
+    ld = m.ld;
+  };
   int cur = 0;
-  for (int i = 0; i < steps && rc == W4Q_OK; ++i) {
-    // A = X X^T
+  for (int i = 0; i < steps && rc == W4Q_OK; ++i, cur ^= 1) {
+    const Split& X = x[cur];
+    // A = X X^T (Y^T Y)
     NtArgs ga = {};
-    ga.a[0] = ga.b[0] = xnh;
-    ga.a[1] = ga.b[1] = xnl;
-    ga.sa = ga.sb = sxn;
+    operand(X, ga.a, ga.sa, ga.lda);
+    operand(X, ga.b, ga.sb, ga.ldb);
     ga.M = ga.N = n;
-    ga.K = kp;
-    ga.lda = ga.ldb = kp;
-    EpiSplit e = {};
+    ga.K = static_cast<int>(l.wide ? l.ld : rows);
+    ga.ka = ga.kb = static_cast<int>(rows);
+    EpiSplit<true> e = {};
     e.beta = kSplitInv;
-    e.oh = e.th = ah;
-    e.ol = e.tl = al;
-    e.ldo = e.ldt = np;
-    e.so = e.st = snn;
-    e.mirror = 1;
-    if ((rc = ns_product(ga, l.gram, 1, e, part, s)) != W4Q_OK) break;
+    e.o = A;
+    rc = l.wide ? ns_product<false, false>(ga, l.gram, 1, e, part, s) : ns_product<true, true>(ga, l.gram, 1, e, part, s);
+    if (rc != W4Q_OK) break;
     // B = b A + c A A
-    NtArgs gb = ga;
-    gb.a[0] = gb.b[0] = ah;
-    gb.a[1] = gb.b[1] = al;
-    gb.sa = gb.sb = snn;
+    NtArgs gb = {};
+    operand(A, gb.a, gb.sa, gb.lda);
+    operand(A, gb.b, gb.sb, gb.ldb);
+    gb.M = gb.N = n;
     gb.K = np;
-    gb.lda = gb.ldb = np;
-    e.ch = ah;
-    e.cl = al;
-    e.ldc = np;
-    e.sc = snn;
+    e.c = A;
     e.alpha = b;
     e.beta = c * kSplitInv;
-    e.oh = e.th = bh;
-    e.ol = e.tl = bl;
-    if ((rc = ns_product(gb, l.poly, 1, e, part, s)) != W4Q_OK) break;
-    // X <- a X + B X
+    e.o = B;
+    if ((rc = ns_product<false, false>(gb, l.poly, 1, e, part, s)) != W4Q_OK) break;
+    // X <- a X + B X (Y <- a Y + Y B)
     NtArgs gx = {};
+    operand(l.wide ? B : X, gx.a, gx.sa, gx.lda);
+    operand(l.wide ? X : B, gx.b, gx.sb, gx.ldb);
+    gx.M = static_cast<int>(rows);
+    gx.N = static_cast<int>(cols);
     gx.K = np;
-    gx.lda = gx.ldb = np;
+    gx.kb = static_cast<int>(rows);
     if (i + 1 < steps) {
-      gx.a[0] = bh;
-      gx.a[1] = bl;
-      gx.sa = snn;
-      gx.b[0] = xth[cur];
-      gx.b[1] = xtl[cur];
-      gx.sb = sxt;
-      gx.M = n;
-      gx.N = k;
-      EpiSplit u = {};
-      u.ch = xnh;
-      u.cl = xnl;
-      u.ldc = kp;
-      u.sc = sxn;
+      EpiSplit<false> u = {};
+      u.c = X;
       u.alpha = a;
       u.beta = kSplitInv;
-      u.oh = xnh;
-      u.ol = xnl;
-      u.ldo = kp;
-      u.so = sxn;
-      u.th = xth[cur ^ 1];
-      u.tl = xtl[cur ^ 1];
-      u.ldt = np;
-      u.st = sxt;
-      rc = ns_product(gx, l.upd, 0, u, part, s);
-      cur ^= 1;
+      u.o = x[cur ^ 1];
+      rc = l.wide ? ns_product<false, true>(gx, l.upd, 0, u, part, s) : ns_product<false, false>(gx, l.upd, 0, u, part, s);
     } else {
       EpiLast u = {};
+      u.x = X;
       u.alpha = a;
       u.beta = kSplitInv;
       u.out = out;
@@ -456,34 +511,8 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
       u.lr = lr;
       u.scale = scale;
       u.wd = wd;
-      if (wide) {
-        gx.a[0] = bh;
-        gx.a[1] = bl;
-        gx.sa = snn;
-        gx.b[0] = xth[cur];
-        gx.b[1] = xtl[cur];
-        gx.sb = sxt;
-        gx.M = n;
-        gx.N = k;
-        u.ch = xnh;
-        u.cl = xnl;
-        u.ldc = kp;
-        u.sc = sxn;
-      } else {
-        gx.a[0] = xth[cur];
-        gx.a[1] = xtl[cur];
-        gx.sa = sxt;
-        gx.b[0] = bh;
-        gx.b[1] = bl;
-        gx.sb = snn;
-        gx.M = k;
-        gx.N = n;
-        u.ch = xth[cur];
-        u.cl = xtl[cur];
-        u.ldc = np;
-        u.sc = sxt;
-      }
-      rc = ns_product(gx, l.last, 0, u, part, s);
+      u.vec = cols % 8 == 0 && at16(w != nullptr ? static_cast<void*>(w) : out);
+      rc = l.wide ? ns_product<false, true>(gx, l.upd, 0, u, part, s) : ns_product<false, false>(gx, l.upd, 0, u, part, s);
     }
   }
   return rc;

@@ -1,22 +1,33 @@
 // nt_gemm.hpp -- the tiled matrix-core product shared by the linear layer's forward and backward
 // pass (linear.hip) and the Newton-Schulz products (muon.hip):
 //
-//   C[b][i][j] = sum_k A[b][i][k] * B[b][j][k],    both operands with k running along their rows,
+//   C[b][i][j] = sum_k A[b](i, k) * B[b](j, k)
 //
-// where an operand is one 16-bit matrix (bf16, or fp16) or two fp16 matrices hi + lo that hold a
-// value in 22 bits: v = hi + lo with hi = RNE(v), lo = RNE(v - hi).  Products of the parts:
-//   1 x 1 parts: hi hi;   2 x 1: lo hi + hi hi;   2 x 2: hi lo + lo hi + hi hi
-// (lo lo is below 2^-22 of the product and is left out), each exact in fp32 and summed in fp32 by
-// the matrix cores.  What becomes of C is the epilogue's (a functor), so that no C is stored
-// and read again.
+// An operand is one 16-bit matrix (bf16, or fp16) or two fp16 matrices hi + lo that hold a value in
+// 22 bits: v = hi + lo with hi = RNE(v), lo = RNE(v - hi).  Products of the parts:
+//   1 x 1 parts: hi hi;   2 x 1: hi hi + lo hi;   2 x 2: hi lo + hi hi + lo hi
+// (lo lo is below 2^-22 of the product; only the small tile adds it, where products are cheap and few
+// terms average the difference out), each exact in fp32 and summed in fp32 by the matrix cores.
+// What becomes of C is the epilogue's (a functor), so that no C is stored and read again.
 //
-// Mapping: BM x BN output tiles, wavefronts of WM x WN (32x32 blocks of
-// v_mfma_f32_32x32x16), stages of 32 k.  Every part's tile of a stage is a 64-byte row per matrix
-// row, copied to LDS by buffer loads straight to LDS, 16-byte chunk c of row r at position
-// c ^ nt_swz(r): the fragment reads (lane l: row l % 32, chunk 2 kk + l / 32) then touch every
-// bank slot once per pass.  NBUF stage buffers; the loads run NBUF - 1 stages ahead, and one
-// barrier per stage both publishes a stage's tiles and frees the buffer of the stage before it.
-// Rows past the operand's end read as zeros (the buffer's bounds), k is a multiple of 32.
+// An operand lies in memory with k along its rows ("along": A[i][k], K a multiple of 32) or across
+// them ("across": A[k][i], any K).  Either is copied to LDS as it lies, by buffer loads straight to
+// LDS, 32 k a stage: along, 64-byte rows with 16-byte chunk c of row r at c ^ nt_swz(r), read in
+// 16-byte fragments; across, rows of the tile's width with chunk c of row k at c ^ nt_tswz(k), read by
+// the transposing LDS read.  Both patterns touch every bank slot once per pass.  So no operand is
+// ever transposed in memory: of the gradients and of X X^T, B X and X^T X each product reads its
+// operands as their producers wrote them.
+//
+// Mapping: BM x BN output tiles, wavefronts of WM x WN (32x32 blocks of v_mfma_f32_32x32x16).
+// NBUF stage buffers; the loads run NBUF - 1 stages ahead, and one barrier per stage both
+// publishes a stage's tiles and frees the buffer of the stage before it.  Rows and k past an
+// operand's end read as zeros (the buffer's bounds); columns past the end of an "across" row read on
+// into the next row and only feed outputs that are never stored.  With three or more buffers the first
+// half of the next stage's fragments is read before the barrier, between the products of the second.
+//
+// Epilogue: a wavefront passes 32 rows x WN columns at a time through its share of the (then idle)
+// LDS and hands the functor 8 consecutive columns of a row per lane, so that everything the epilogue
+// reads and writes moves in 16-byte pieces; what it reads is loaded one strip ahead.
 //
 // Work split: the (tile, stage) iterations of all tiles lie on one line, cut into nblk equal
 // ranges, one per workgroup.  A range that covers a whole tile ends in the epilogue; partial tiles
@@ -24,26 +35,35 @@
 // depend on timing).  With chunk = stages per tile this is one tile per workgroup and no scratch.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace w4q {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
-// position of 16-byte chunk c in row r (64-byte rows): see gemm.hip for the LDS passes this suits
+// position of 16-byte chunk c in 64-byte row r: see gemm.hip for the LDS passes this suits
 __device__ __forceinline__ int nt_swz(int r) { return (((r >> 1) ^ (r >> 4)) & 1) | ((r >> 1) & 2); }
+// position mask of a chunk of k row t, for rows of `width` values: a transposing read of 16 lanes
+// covers 4 consecutive k x 2 chunks and one of 32 lanes 4 k x 4 chunks, which these masks spread over
+// distinct slots modulo 128 and 256 bytes
+template <int width>
+__device__ __forceinline__ int nt_tswz(int t) {
+  return width == 64 ? 2 * (t & 3) : (0xCA60 >> (4 * (t & 3))) & 15;
+}
 
 struct NtArgs {
   const uint16_t* a[2];
   const uint16_t* b[2];
   int64_t sa, sb;     // elements between the batches of A and B
-  int M, N, K;        // K a multiple of 32
-  int lda, ldb;       // elements per row, >= K, multiples of 8
+  int M, N, K;        // K a multiple of 32 unless both operands lie across
+  int ka, kb;         // k rows that A, B really have, where they lie across (K up to the next 32 is zero)
+  int lda, ldb;       // elements per row, multiples of 8
   int tm, tn;         // tiles along M and N
   int tri;            // 1: M == N and only tiles with row tile >= column tile
   int per_batch;      // tiles of one batch
-  int S;              // stages per tile (K / 32)
+  int S;              // stages per tile
   int total;          // iterations (batches * per_batch * S)
   int chunk, nblk, per_xcd;
   float* ws;
@@ -69,10 +89,11 @@ __device__ __forceinline__ void nt_tile(const NtArgs& g, int t, int& batch, int&
   }
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int PA_, int PB_, bool F16_, int NBUF_>
+template <int BM_, int BN_, int WM_, int WN_, int PA_, int PB_, bool F16_, bool AT_, bool BT_, int NBUF_,
+          bool LOLO_ = false>
 struct NtCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PA = PA_, PB = PB_, NBUF = NBUF_;
-  static constexpr bool F16 = F16_;
+  static constexpr bool F16 = F16_, AT = AT_, BT = BT_, LOLO = LOLO_;  // AT, BT: operand lies across
   static constexpr int kWavesM = BM / WM, kWavesN = BN / WN, kWaves = kWavesM * kWavesN;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int MB = WM / 32, NB = WN / 32;
@@ -82,8 +103,12 @@ struct NtCfg {
   static constexpr int kStage = PA * kBytesA + PB * kBytesB;
   static constexpr int kLds = NBUF * kStage;
   static constexpr int kTileElems = BM * BN;
+  static constexpr int kPitch = WN + 4;                               // floats per row of an epilogue strip
+  static constexpr int kReads = PA * MB * (AT ? 2 : 1) + PB * NB * (BT ? 2 : 1);  // LDS reads per step
+  static constexpr int kMma = MB * NB * (PA + PB - 1 + (LOLO ? 1 : 0));           // products per step
   static_assert(LA >= 1 && LB >= 1 && LA <= 2 && LB <= 2, "1 or 2 loads per wave and part");
-  static_assert(kLds <= 160 * 1024, "LDS");
+  static_assert(kLds <= 160 * 1024 && kLds / kWaves >= 32 * kPitch * 4, "LDS");
+  static_assert(!LOLO || (PA == 2 && PB == 2), "parts");
 };
 
 template <bool F16>
@@ -94,10 +119,75 @@ __device__ __forceinline__ f32x16 nt_mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+#define W4Q_TR_LDS(p) ((__attribute__((address_space(3))) v4i16*)(p))
+
 // partial-tile layout: wavefront, block, 16-byte quarter, lane (1 KB per store instruction)
 template <class C>
 __device__ __forceinline__ int64_t nt_part_off(int w, int blk, int q, int lane) {
   return static_cast<int64_t>(((w * (C::MB * C::NB) + blk) * 4 + q) * 256 + 4 * lane);
+}
+
+// ---------------------------------------------------------------------------- epilogue strips
+// A strip is 32 rows x WN columns of a wavefront's tile.  Lane l takes 8 columns from 8 (l % (WN / 8)) of
+// rows l / (WN / 8) + kRows i.  The functor gives, for 8 columns of one row:
+//   Pre load(g, batch, row, col)                     what the epilogue reads there
+//   void store(g, batch, row, col, v[8], pre)        writes the outputs; leaves in v what a mirrored
+//                                                    store shall write
+//   kMirror, void store_t(g, batch, col, row, v[8])  symmetric results: 8 rows of one column
+template <class C>
+struct NtStrip {
+  static constexpr int kLanes = C::WN / 8;     // lanes per row
+  static constexpr int kRows = 64 / kLanes;    // rows per pass
+  static constexpr int kPasses = 32 / kRows;
+};
+
+template <class C, class Epi>
+__device__ __forceinline__ void nt_strip_load(const NtArgs& g, const Epi& epi, int batch, int row0, int col0, int lane,
+                                              typename Epi::Pre (&pre)[NtStrip<C>::kPasses]) {
+  using S = NtStrip<C>;
+#pragma unroll
+  for (int i = 0; i < S::kPasses; ++i)
+    pre[i] = epi.load(g, batch, row0 + lane / S::kLanes + S::kRows * i, col0 + 8 * (lane % S::kLanes));
+}
+
+template <class C, class Epi>
+__device__ __forceinline__ void nt_strip_store(const NtArgs& g, const Epi& epi, int batch, int row0, int col0, bool diag,
+                                               const f32x16 (&acc)[C::NB], int lane, float* buf,
+                                               const typename Epi::Pre (&pre)[NtStrip<C>::kPasses]) {
+  using S = NtStrip<C>;
+  // accumulator layout: lane l, register r -> row 8(r/4) + 4(l/32) + r%4, column l%32
+#pragma unroll
+  for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      buf[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * C::kPitch + 32 * j + (lane & 31)] = acc[j][r];
+  asm volatile("" ::: "memory");  // the wavefront's own LDS operations stay in order
+#pragma unroll
+  for (int i = 0; i < S::kPasses; ++i) {
+    const int rl = lane / S::kLanes + S::kRows * i, cl = 8 * (lane % S::kLanes);
+    float* p = buf + rl * C::kPitch + cl;
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    epi.store(g, batch, row0 + rl, col0 + cl, v, pre[i]);
+    if constexpr (Epi::kMirror) {
+      *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  }
+  if constexpr (Epi::kMirror) {
+    if (!diag) {
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < C::WN / 16; ++i) {
+        const int cl = 16 * i + (lane >> 2), rl = 8 * (lane & 3);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = buf[(rl + e) * C::kPitch + cl];
+        epi.store_t(g, batch, col0 + cl, row0 + rl, v);
+      }
+    }
+  }
+  asm volatile("" ::: "memory");
 }
 
 template <class C, class Epi>
@@ -113,32 +203,59 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
   const int lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wid / C::kWavesN, wn = wid % C::kWavesN;
-  const int fr = lane & 31, fh = lane >> 5;
   const uint32_t lds0 = lds_addr(lds);
 
+  // byte offsets of this lane's loads of a stage: load u of a part fills 1 KB of the part's tile
+  auto load_off = [&](int u, int ld, auto across, auto width) {
+    if constexpr (decltype(across)::value) {
+      constexpr int W = decltype(width)::value, CPR = W / 8, RPL = 64 / CPR;  // chunks per row, rows per load
+      const int t = u * RPL + lane / CPR;
+      return t * ld * 2 + 16 * ((lane % CPR) ^ nt_tswz<W>(t));
+    } else {
+      const int r = 16 * u + (lane >> 2);
+      return r * ld * 2 + 16 * ((lane & 3) ^ nt_swz(r));
+    }
+  };
   int avo[C::LA], bvo[C::LB];
 #pragma unroll
-  for (int q = 0; q < C::LA; ++q) {
-    const int r = 16 * (wid * C::LA + q) + (lane >> 2);
-    avo[q] = r * g.lda * 2 + 16 * ((lane & 3) ^ nt_swz(r));
-  }
+  for (int q = 0; q < C::LA; ++q)
+    avo[q] = load_off(wid * C::LA + q, g.lda, std::bool_constant<C::AT>{}, std::integral_constant<int, C::BM>{});
 #pragma unroll
-  for (int q = 0; q < C::LB; ++q) {
-    const int r = 16 * (wid * C::LB + q) + (lane >> 2);
-    bvo[q] = r * g.ldb * 2 + 16 * ((lane & 3) ^ nt_swz(r));
-  }
-  // byte offsets of this lane's fragments within a part's tile, step 0; step 1 flips bit 5
+  for (int q = 0; q < C::LB; ++q)
+    bvo[q] = load_off(wid * C::LB + q, g.ldb, std::bool_constant<C::BT>{}, std::integral_constant<int, C::BN>{});
+  // byte offsets of this lane's fragments within a part's tile, first step of 16 k
+  auto read_off = [&](int r0, auto across, auto width) {
+    if constexpr (decltype(across)::value) {
+      constexpr int W = decltype(width)::value;
+      // 16-lane group rg, lane rj in it: k 8 (rg / 2) + rj / 4 (+ 4 in the second read), values
+      // 16 (rg % 2) + 4 (rj % 4); it receives value 16 (rg % 2) + rj of four consecutive k
+      const int rg = lane >> 4, rj = lane & 15;
+      const int t = 8 * (rg >> 1) + (rj >> 2);
+      const int c = r0 / 8 + 2 * (rg & 1) + ((rj >> 1) & 1);
+      return t * (2 * W) + 16 * (c ^ nt_tswz<W>(t)) + 8 * (rj & 1);
+    } else {
+      const int r = r0 + (lane & 31);
+      return r * 64 + 16 * ((lane >> 5) ^ nt_swz(r));
+    }
+  };
   int aro[C::MB], bro[C::NB];
 #pragma unroll
-  for (int i = 0; i < C::MB; ++i) {
-    const int r = wm * C::WM + 32 * i + fr;
-    aro[i] = r * 64 + 16 * (fh ^ nt_swz(r));
-  }
+  for (int i = 0; i < C::MB; ++i)
+    aro[i] = read_off(wm * C::WM + 32 * i, std::bool_constant<C::AT>{}, std::integral_constant<int, C::BM>{});
 #pragma unroll
-  for (int j = 0; j < C::NB; ++j) {
-    const int r = wn * C::WN + 32 * j + fr;
-    bro[j] = r * 64 + 16 * (fh ^ nt_swz(r));
-  }
+  for (int j = 0; j < C::NB; ++j)
+    bro[j] = read_off(wn * C::WN + 32 * j, std::bool_constant<C::BT>{}, std::integral_constant<int, C::BN>{});
+  auto read_frag = [&](const uint8_t* tile, int off, int kk, auto across, auto width) -> u32x4 {
+    if constexpr (decltype(across)::value) {
+      constexpr int W = decltype(width)::value;
+      const uint8_t* p = tile + off + kk * 16 * 2 * W;
+      const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(W4Q_TR_LDS(p));
+      const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(W4Q_TR_LDS(p + 4 * 2 * W));
+      return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *reinterpret_cast<const u32x4*>(tile + (off ^ (32 * kk)));
+    }
+  };
 
   int it = it_begin;
   while (it < it_end) {
@@ -148,35 +265,41 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     int batch, ti, tj;
     nt_tile(g, t, batch, ti, tj);
     const int m0 = ti * C::BM, n0 = tj * C::BN;
-    const int arows = g.M - m0 < C::BM ? g.M - m0 : C::BM;
-    const int brows = g.N - n0 < C::BN ? g.N - n0 : C::BN;
-    const int abytes = arows * g.lda * 2, bbytes = brows * g.ldb * 2;
-    const int64_t ao = batch * g.sa + static_cast<int64_t>(m0) * g.lda;
-    const int64_t bo = batch * g.sb + static_cast<int64_t>(n0) * g.ldb;
+    const uint16_t* abase[2] = {g.a[0] + batch * g.sa, C::PA == 2 ? g.a[1] + batch * g.sa : nullptr};
+    const uint16_t* bbase[2] = {g.b[0] + batch * g.sb, C::PB == 2 ? g.b[1] + batch * g.sb : nullptr};
 
     // loads of stage s into buffer `buf` (past the range: empty loads, which write zeros)
+    auto issue_part = [&](const uint16_t* base, int s, bool live, int r0, int rows, int ld, uint32_t dst, auto across,
+                          auto width, int krows, const auto& vo) {
+      constexpr int W = decltype(width)::value;
+      int64_t off;
+      int bytes;
+      if constexpr (decltype(across)::value) {
+        const int left = krows - 32 * s;
+        off = static_cast<int64_t>(32 * s) * ld + r0;
+        bytes = ((left < 32 ? left : 32) * ld - r0) * 2;
+      } else {
+        const int left = rows - r0;
+        off = static_cast<int64_t>(r0) * ld + 32 * s;
+        bytes = ((left < W ? left : W) * ld - 32 * s) * 2;
+      }
+      const v4i32 rs = buffer_rsrc(base + (live ? off : 0), live ? bytes : 0);
+      if constexpr (sizeof(vo) == 8)
+        dma_x2(dst + wid * 2048, rs, vo[0], vo[1]);
+      else
+        dma_x1(dst + wid * 1024, rs, vo[0]);
+    };
     auto issue = [&](int s, int buf) {
       const bool live = s < s1;
-      const int so = live ? s * 32 : 0;
       uint32_t dst = lds0 + buf * C::kStage;
 #pragma unroll
-      for (int p = 0; p < C::PA; ++p) {
-        const v4i32 rs = buffer_rsrc(g.a[p] + ao + so, live ? abytes - so * 2 : 0);
-        if constexpr (C::LA == 2)
-          dma_x2(dst + wid * 2048, rs, avo[0], avo[1]);
-        else
-          dma_x1(dst + wid * 1024, rs, avo[0]);
-        dst += C::kBytesA;
-      }
+      for (int p = 0; p < C::PA; ++p, dst += C::kBytesA)
+        issue_part(abase[p], s, live, m0, g.M, g.lda, dst, std::bool_constant<C::AT>{},
+                   std::integral_constant<int, C::BM>{}, g.ka, avo);
 #pragma unroll
-      for (int p = 0; p < C::PB; ++p) {
-        const v4i32 rs = buffer_rsrc(g.b[p] + bo + so, live ? bbytes - so * 2 : 0);
-        if constexpr (C::LB == 2)
-          dma_x2(dst + wid * 2048, rs, bvo[0], bvo[1]);
-        else
-          dma_x1(dst + wid * 1024, rs, bvo[0]);
-        dst += C::kBytesB;
-      }
+      for (int p = 0; p < C::PB; ++p, dst += C::kBytesB)
+        issue_part(bbase[p], s, live, n0, g.N, g.ldb, dst, std::bool_constant<C::BT>{},
+                   std::integral_constant<int, C::BN>{}, g.kb, bvo);
     };
 
     f32x16 acc[C::MB][C::NB];
@@ -187,73 +310,105 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-    auto step = [&](const uint8_t* base, int kk) {
-      const uint8_t* pa = base;
-      const uint8_t* pb = base + C::PA * C::kBytesA;
+    struct Frags {
       u32x4 a[C::PA][C::MB], b[C::PB][C::NB];
+    };
+    auto load = [&](int buf, int kk, Frags& f) {
+      const uint8_t* pa = lds + buf * C::kStage;
+      const uint8_t* pb = pa + C::PA * C::kBytesA;
+#pragma unroll
+      for (int p = C::PB - 1; p >= 0; --p)
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j)
+          f.b[p][j] = read_frag(pb + p * C::kBytesB, bro[j], kk, std::bool_constant<C::BT>{},
+                                std::integral_constant<int, C::BN>{});
 #pragma unroll
       for (int p = 0; p < C::PA; ++p)
 #pragma unroll
         for (int i = 0; i < C::MB; ++i)
-          a[p][i] = *reinterpret_cast<const u32x4*>(pa + p * C::kBytesA + (aro[i] ^ (32 * kk)));
-#pragma unroll
-      for (int p = 0; p < C::PB; ++p)
-#pragma unroll
-        for (int j = 0; j < C::NB; ++j)
-          b[p][j] = *reinterpret_cast<const u32x4*>(pb + p * C::kBytesB + (bro[j] ^ (32 * kk)));
-      if constexpr (C::PB == 2) {
-#pragma unroll
-        for (int i = 0; i < C::MB; ++i)
-#pragma unroll
-          for (int j = 0; j < C::NB; ++j) acc[i][j] = nt_mfma<C::F16>(a[0][i], b[1][j], acc[i][j]);
-      }
-      if constexpr (C::PA == 2) {
-#pragma unroll
-        for (int i = 0; i < C::MB; ++i)
-#pragma unroll
-          for (int j = 0; j < C::NB; ++j) acc[i][j] = nt_mfma<C::F16>(a[1][i], b[0][j], acc[i][j]);
-      }
+          f.a[p][i] = read_frag(pa + p * C::kBytesA, aro[i], kk, std::bool_constant<C::AT>{},
+                                std::integral_constant<int, C::BM>{});
+    };
+    auto mma_parts = [&](const u32x4 (&a)[C::MB], const u32x4 (&b)[C::NB]) {
 #pragma unroll
       for (int i = 0; i < C::MB; ++i)
 #pragma unroll
-        for (int j = 0; j < C::NB; ++j) acc[i][j] = nt_mfma<C::F16>(a[0][i], b[0][j], acc[i][j]);
+        for (int j = 0; j < C::NB; ++j) acc[i][j] = nt_mfma<C::F16>(a[i], b[j], acc[i][j]);
     };
-
+    auto mma = [&](const Frags& f) {
+      if constexpr (C::PB == 2) mma_parts(f.a[0], f.b[1]);
+      mma_parts(f.a[0], f.b[0]);
+      if constexpr (C::PA == 2) mma_parts(f.a[1], f.b[0]);
+      if constexpr (C::LOLO) mma_parts(f.a[1], f.b[1]);
+    };
+    // the next step's LDS reads spread between this step's products
+    auto pattern = [&]() {
+      constexpr int per = C::kMma / C::kReads;
+      if constexpr (per >= 1) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) issue(s0 + d, d);
-    int buf = 0;
-    for (int s = s0; s < s1; ++s) {
-      // this wave's loads of stage s have landed and its reads of the stage before are done;
-      // after the barrier that holds for every wave
+        for (int i = 0; i < C::kReads; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, per, 0);  // MFMA
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // LDS read
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, C::kMma - per * C::kReads, 0);
+      }
+    };
+    // this wave's loads but the youngest n have landed and its LDS reads are done; after the barrier
+    // that holds for every wave
+    auto sync = [&](auto n) {
       __builtin_amdgcn_sched_barrier(0);
       asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((D - 1) * C::kOps));
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(decltype(n)::value));
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      const int nb = buf + D >= C::NBUF ? buf + D - C::NBUF : buf + D;
-      issue(s + D, nb);
-      const uint8_t* base = lds + buf * C::kStage;
-      step(base, 0);
-      step(base, 1);
-      buf = buf + 1 == C::NBUF ? 0 : buf + 1;
+    };
+    auto next = [](int buf, int n) { return buf + n >= C::NBUF ? buf + n - C::NBUF : buf + n; };
+
+    Frags f0, f1;
+#pragma unroll
+    for (int d = 0; d < D; ++d) issue(s0 + d, d);
+    int buf = 0;
+    if constexpr (D >= 2) {
+      sync(std::integral_constant<int, (D - 1) * C::kOps>{});  // stage s0
+      load(0, 0, f0);
+      for (int s = s0; s < s1; ++s) {
+        // stages s and s + 1 have landed; the buffer of s - 1 is free
+        sync(std::integral_constant<int, (D - 2) * C::kOps>{});
+        issue(s + D, next(buf, D));
+        load(buf, 1, f1);
+        mma(f0);
+        pattern();
+        buf = next(buf, 1);
+        load(buf, 0, f0);  // (past the range: a buffer of zeros, never used)
+        mma(f1);
+        pattern();
+      }
+    } else {
+      for (int s = s0; s < s1; ++s) {
+        sync(std::integral_constant<int, 0>{});  // stage s has landed; the other buffer is free
+        issue(s + 1, buf ^ 1);
+        load(buf, 0, f0);
+        load(buf, 1, f1);
+        mma(f0);
+        mma(f1);
+        buf ^= 1;
+      }
     }
-    // nothing of this tile is in flight or still being read when the next tile's loads are issued
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
+    // nothing is in flight or still being read when the buffers are used for other things
+    sync(std::integral_constant<int, 0>{});
 
     if (s0 == 0 && s1 == g.S) {
+      float* strip = reinterpret_cast<float*>(lds + wid * (C::kLds / C::kWaves));
+      const int row0 = m0 + wm * C::WM, col0 = n0 + wn * C::WN;
+      typename Epi::Pre pre[2][NtStrip<C>::kPasses];
+      nt_strip_load<C>(g, epi, batch, row0, col0, lane, pre[0]);
 #pragma unroll
-      for (int i = 0; i < C::MB; ++i)
-#pragma unroll
-        for (int j = 0; j < C::NB; ++j) {
-          epi(g, batch, m0 + wm * C::WM + 32 * i, n0 + wn * C::WN + 32 * j, ti == tj, acc[i][j], lane);
-          asm volatile("" ::: "memory");
-        }
+      for (int i = 0; i < C::MB; ++i) {
+        if (i + 1 < C::MB) nt_strip_load<C>(g, epi, batch, row0 + 32 * (i + 1), col0, lane, pre[(i + 1) & 1]);
+        nt_strip_store<C>(g, epi, batch, row0 + 32 * i, col0, ti == tj, acc[i], lane, strip, pre[i & 1]);
+      }
+      if (it + (s1 - s0) < it_end) sync(std::integral_constant<int, 0>{});  // the next tile's loads reuse the LDS
     } else {
       float* slot = g.ws + static_cast<int64_t>(2 * lb + (it == it_begin ? 0 : 1)) * C::kTileElems;
 #pragma unroll
@@ -272,37 +427,43 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
 }
 
 // Tiles whose stages were spread over several workgroups: the partial tiles summed in k order,
-// then the epilogue.  One wavefront per 32x32 block (four to a workgroup).
+// then the epilogue.  One wavefront per strip of 32 rows x WN columns.
 template <class C, class Epi>
-__global__ __launch_bounds__(256) void nt_fixup_kernel(const NtArgs g, const Epi epi) {
-  constexpr int kBlocks = C::kWaves * C::MB * C::NB;  // 32x32 blocks of a tile, a multiple of 4
-  static_assert(kBlocks % 4 == 0, "four blocks per workgroup");
-  const int t = static_cast<int>(blockIdx.x) / (kBlocks / 4);
-  const int lane = threadIdx.x & 63;
-  const int blk = 4 * (static_cast<int>(blockIdx.x) % (kBlocks / 4)) +
-                  __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+__global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi epi) {
+  __shared__ __attribute__((aligned(16))) float strip[32 * C::kPitch];
+  constexpr int kStrips = C::kWaves * C::MB;  // strips of a tile
+  const int t = static_cast<int>(blockIdx.x) / kStrips;
   const int64_t b0 = static_cast<int64_t>(t) * g.S;
   const int first = static_cast<int>(b0 / g.chunk);
   const int last = static_cast<int>((b0 + g.S - 1) / g.chunk);
   if (first == last) return;  // one workgroup held the whole tile
-  const int wid = blk / (C::MB * C::NB), ij = blk % (C::MB * C::NB);
-  f32x16 v;
+  const int lane = threadIdx.x & 63;
+  const int si = static_cast<int>(blockIdx.x) % kStrips;
+  const int wid = si / C::MB, i = si % C::MB;
+  int batch, ti, tj;
+  nt_tile(g, t, batch, ti, tj);
+  const int row0 = ti * C::BM + (wid / C::kWavesN) * C::WM + 32 * i;
+  const int col0 = tj * C::BN + (wid % C::kWavesN) * C::WN;
+  typename Epi::Pre pre[NtStrip<C>::kPasses];
+  nt_strip_load<C>(g, epi, batch, row0, col0, lane, pre);
+  f32x16 v[C::NB];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) v[r] = 0.0f;
+  for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v[j][r] = 0.0f;
   for (int b = first; b <= last; ++b) {
     const int slot = 2 * b + (static_cast<int64_t>(b) * g.chunk >= b0 ? 0 : 1);
     const float* p = g.ws + static_cast<int64_t>(slot) * C::kTileElems;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(p + nt_part_off<C>(wid, ij, q, lane));
+    for (int j = 0; j < C::NB; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * q + e] += x[e];
-    }
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(p + nt_part_off<C>(wid, i * C::NB + j, q, lane));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][4 * q + e] += x[e];
+      }
   }
-  int batch, ti, tj;
-  nt_tile(g, t, batch, ti, tj);
-  epi(g, batch, ti * C::BM + (wid / C::kWavesN) * C::WM + 32 * (ij / C::NB),
-      tj * C::BN + (wid % C::kWavesN) * C::WN + 32 * (ij % C::NB), ti == tj, v, lane);
+  nt_strip_store<C>(g, epi, batch, row0, col0, ti == tj, v, lane, strip, pre);
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -322,7 +483,7 @@ inline NtPlan nt_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, 
   p.tm = (M + BM - 1) / BM;
   p.tn = (N + BN - 1) / BN;
   p.per_batch = tri ? p.tm * (p.tm + 1) / 2 : p.tm * p.tn;
-  p.S = K / 32;
+  p.S = (K + 31) / 32;
   const int64_t tiles = batch * p.per_batch;
   p.total = tiles * p.S;
   p.chunk = p.S;
@@ -354,9 +515,9 @@ int nt_launch(NtArgs g, const NtPlan& p, int tri, const Epi& epi, void* ws, hipS
   hipLaunchKernelGGL((nt_kernel<C, Epi>), dim3(static_cast<unsigned>(8 * g.per_xcd)), dim3(C::kThreads), 0, s, g, epi);
   int rc = w4q_launch_status();
   if (rc == W4Q_OK && p.ws != 0) {
-    constexpr int per_tile = C::kWaves * C::MB * C::NB / 4;
+    constexpr int per_tile = C::kWaves * C::MB;
     const int64_t tiles = p.total / p.S;
-    hipLaunchKernelGGL((nt_fixup_kernel<C, Epi>), dim3(static_cast<unsigned>(tiles * per_tile)), dim3(256), 0, s, g, epi);
+    hipLaunchKernelGGL((nt_fixup_kernel<C, Epi>), dim3(static_cast<unsigned>(tiles * per_tile)), dim3(64), 0, s, g, epi);
     rc = w4q_launch_status();
   }
   return rc;
