@@ -32,7 +32,7 @@ constexpr float kDactMax = 1.13f; // |act'| <= 1.1290 (gelu), 1.0999 (silu), 1 (
 
 // ------------------------------------------------------------------------------ epilogues
 struct EpiLinear {
-  static constexpr bool kMirror = false;
+  static constexpr bool kMirror = false, kAhead = true;
   struct Pre {
     u32x4 r0, r1;
   };
@@ -96,7 +96,7 @@ struct EpiLinear {
 
 // a gradient product: the operands' powers of two taken back, stored as fp32 or bf16
 struct EpiGrad {
-  static constexpr bool kMirror = false;
+  static constexpr bool kMirror = false, kAhead = true;
   struct Pre {
     int e;
   };
@@ -229,7 +229,7 @@ struct DzArgs {
   const uint16_t* z;
   int act, vec;
   int64_t m, n, np;
-  uint16_t *hi, *lo;  // null: not wanted (the sums alone)
+  uint16_t *hi, *both;  // null: not wanted
   float* bsum;        // [ceil(m / 64)][n] or null
   const float* parts;
   int* exp_out;
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += v[j];
-    if (a.hi == nullptr) continue;
+    if (!kSplit && a.hi == nullptr) continue;
     const int64_t at = row * a.np + col;
     if constexpr (kSplit) {
       u32x4 h, l;
@@ -303,8 +303,12 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
         h[j] = hb[0] | (hb[1] << 16);
         l[j] = lb[0] | (lb[1] << 16);
       }
-      *reinterpret_cast<u32x4*>(a.hi + at) = h;
-      if (a.lo != nullptr) *reinterpret_cast<u32x4*>(a.lo + at) = l;
+      if (a.hi != nullptr) *reinterpret_cast<u32x4*>(a.hi + at) = h;
+      if (a.both != nullptr) {  // the split matrix: the parts of 32 columns side by side
+        uint16_t* q = a.both + row * (2 * a.np) + (col >> 5) * 64 + (col & 31);
+        *reinterpret_cast<u32x4*>(q) = h;
+        *reinterpret_cast<u32x4*>(q + 32) = l;
+      }
     } else {
       *reinterpret_cast<u32x4*>(a.hi + at) = raw;
     }
@@ -334,26 +338,26 @@ __global__ __launch_bounds__(256) void bias_kernel(const float* __restrict__ bsu
 
 // ------------------------------------------------------------------------------ products
 template <int PA, bool F16, bool AT, bool BT>
-using Big = NtCfg<256, 256, 128, 64, PA, 1, F16, AT, BT, PA == 1 ? 4 : 3>;
+using Big = NtCfg<256, 256, 128, 64, PA, 1, F16, AT, BT>;
 template <int PA, bool F16, bool AT, bool BT>
-using Mid = NtCfg<128, 128, 64, 64, PA, 1, F16, AT, BT, PA == 1 ? 4 : 3>;
+using Mid = NtCfg<128, 128, 64, 64, PA, 1, F16, AT, BT>;
 template <int PA, bool F16, bool AT, bool BT>
-using Small = NtCfg<64, 64, 32, 32, PA, 1, F16, AT, BT, 4>;
+using Small = NtCfg<64, 64, 32, 32, PA, 1, F16, AT, BT>;
 
 struct LinPlan {
   int kind;  // 0 Big, 1 Mid, 2 Small
   NtPlan p;
 };
 // Tile size by how many tiles there are: the largest one that still gives most compute units work.
-LinPlan lin_plan(int64_t M, int64_t N, int64_t K) {
+LinPlan lin_plan(int64_t M, int64_t N, int64_t K, int BK) {
   LinPlan r;
-  r.p = nt_plan(1, M, N, K, false, 256, 256, kNtCus);
+  r.p = nt_plan(1, M, N, K, false, 256, 256, BK, kNtCus);
   r.kind = 0;
   if (r.p.per_batch >= 96) return r;
-  r.p = nt_plan(1, M, N, K, false, 128, 128, 2 * kNtCus);
+  r.p = nt_plan(1, M, N, K, false, 128, 128, BK, 2 * kNtCus);
   r.kind = 1;
   if (r.p.per_batch >= 128) return r;
-  r.p = nt_plan(1, M, N, K, false, 64, 64, 4 * kNtCus);
+  r.p = nt_plan(1, M, N, K, false, 64, 64, BK, 4 * kNtCus);
   r.kind = 2;
   return r;
 }
@@ -382,7 +386,7 @@ struct BwdLayout {
   bool direct;       // the products read dy as it lies
   int64_t np, mt;
   LinPlan px, pw;
-  size_t parts, exps, hi, lo, x16, w16, bsum, part, total;
+  size_t parts, exps, hi, both, x16, w16, bsum, part, total;
 };
 BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   BwdLayout l;
@@ -390,8 +394,8 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   l.np = up32(n);
   l.mt = (m + kDzRows - 1) / kDzRows;
   l.direct = !l.split && l.np == n;
-  l.px = lin_plan(m, k, l.np);
-  l.pw = lin_plan(n, k, m);
+  l.px = lin_plan(m, k, l.np, 64);
+  l.pw = lin_plan(n, k, m, l.split ? 32 : 64);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -401,7 +405,7 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   l.parts = take(l.split ? 3 * kAmaxBlocks * sizeof(float) : 0);
   l.exps = take(l.split ? 3 * sizeof(int) : 0);
   l.hi = take(l.direct ? 0 : size_t(2) * m * l.np);
-  l.lo = take(l.split ? size_t(2) * m * l.np : 0);
+  l.both = take(l.split ? size_t(4) * m * l.np : 0);
   l.x16 = take(l.split ? size_t(2) * m * k : 0);
   l.w16 = take(l.split ? size_t(2) * n * k : 0);
   l.bsum = take(sizeof(float) * l.mt * n);
@@ -414,7 +418,7 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
 // row lengths whose 256-row tiles stay within 32-bit buffer offsets, and iteration counts of the products
 bool fits(int64_t M, int64_t N, int64_t K) {
   if (M > 0x3FFFFFFF || N > 0x3FFFFFFF || K > (1 << 21)) return false;
-  return lin_plan(M, N, K).p.total <= 0x3FFFFFFF;
+  return lin_plan(M, N, K, 32).p.total <= 0x3FFFFFFF;
 }
 
 }  // namespace
@@ -426,10 +430,10 @@ bool w4q_linear_fits(int64_t m, int64_t d_out, int64_t d_in, bool backward) {
   if (!backward) return fits(m, d_out, d_in);
   // one workgroup per 64 rows in the pass over dz; 32 rows of an operand within 32-bit buffer offsets
   if ((m + kDzRows - 1) / kDzRows > 65535 || d_in > (1 << 21)) return false;
-  return fits(m, d_in, up32(d_out)) && lin_plan(d_out, d_in, m).p.total <= 0x3FFFFFFF;
+  return fits(m, d_in, up32(d_out)) && lin_plan(d_out, d_in, m, 32).p.total <= 0x3FFFFFFF;
 }
 
-size_t w4q_linear_fwd_workspace(int64_t m, int64_t d_out, int64_t d_in) { return lin_plan(m, d_out, d_in).p.ws; }
+size_t w4q_linear_fwd_workspace(int64_t m, int64_t d_out, int64_t d_in) { return lin_plan(m, d_out, d_in, 64).p.ws; }
 size_t w4q_linear_bwd_workspace(int64_t m, int64_t d_out, int64_t d_in, int dy_f32, int act) {
   return bwd_layout(m, d_out, d_in, dy_f32, act).total;
 }
@@ -437,11 +441,11 @@ size_t w4q_linear_bwd_workspace(int64_t m, int64_t d_out, int64_t d_in, int dy_f
 int w4q_launch_linear_fwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,
                           const float* bias, int act, const void* res, uint16_t* z, void* y, int y_dtype, void* ws,
                           size_t ws_bytes, hipStream_t s) {
-  LinPlan p = lin_plan(m, d_out, d_in);
+  LinPlan p = lin_plan(m, d_out, d_in, 64);
   fit_plan(p, ws != nullptr ? ws_bytes : 0);
   NtArgs g = {};
-  g.a[0] = x;
-  g.b[0] = w_hat;
+  g.a = x;
+  g.b = w_hat;
   g.M = static_cast<int>(m);
   g.N = static_cast<int>(d_out);
   g.K = g.lda = g.ldb = static_cast<int>(d_in);
@@ -474,8 +478,8 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   const bool need = products && !l.direct;
   if (need || db != nullptr) {
     const bool vec = d_out % 8 == 0 && at16(z);
-    const DzArgs a = {dy, dy_f32, z, act, vec ? 1 : 0, m, d_out, l.np, need ? u16(l.hi) : nullptr,
-                      l.split && dw != nullptr ? u16(l.lo) : nullptr, bsum, parts, exps};
+    const DzArgs a = {dy, dy_f32, z, act, vec ? 1 : 0, m, d_out, l.np, need && (dx != nullptr || !l.split) ? u16(l.hi) : nullptr,
+                      l.split && dw != nullptr ? u16(l.both) : nullptr, bsum, parts, exps};
     const dim3 grid(static_cast<unsigned>((l.np + 255) / 256), static_cast<unsigned>(l.mt));
     if (l.split && need)
       hipLaunchKernelGGL(dz_kernel<true>, grid, dim3(256), 0, s, a);
@@ -491,8 +495,8 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   const bool vec = at16(dx) && at16(dw);  // (rows of d_in, a multiple of 32, values)
   if (dx != nullptr) {  // dx [m][d_in] = dz W: dz along n, W across
     NtArgs g = {};
-    g.a[0] = hi;
-    g.b[0] = l.split ? u16(l.w16) : w_hat;
+    g.a = hi;
+    g.b = l.split ? u16(l.w16) : w_hat;
     g.M = static_cast<int>(m);
     g.N = g.ldb = static_cast<int>(d_in);
     g.K = g.lda = static_cast<int>(l.np);
@@ -503,12 +507,11 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   }
   if (dw != nullptr) {  // dW [d_out][d_in] = dz^T x: both across
     NtArgs g = {};
-    g.a[0] = hi;
-    g.a[1] = u16(l.lo);
-    g.b[0] = l.split ? u16(l.x16) : x;
+    g.a = l.split ? u16(l.both) : hi;
+    g.b = l.split ? u16(l.x16) : x;
     g.M = static_cast<int>(d_out);
     g.N = g.ldb = static_cast<int>(d_in);
-    g.lda = static_cast<int>(l.np);
+    g.lda = static_cast<int>(l.split ? 2 * l.np : l.np);
     g.K = g.ka = g.kb = static_cast<int>(m);
     const EpiGrad e = {exps, l.split ? exps + 1 : nullptr, dw, 0, vec ? 1 : 0};
     rc = l.split ? lin_product<2, true, true, true>(g, l.pw, e, part, s) : lin_product<1, false, true, true>(g, l.pw, e, part, s);

@@ -58,18 +58,31 @@ __device__ __forceinline__ void join8(const u32x4& h, const u32x4& l, float (&v)
   }
 }
 
-// a split matrix [rows][ld] per batch, ld a multiple of 32
+// a split matrix per batch (nt_gemm.hpp): rows of ld columns, ld a multiple of 32; the parts of 32
+// columns side by side
 struct Split {
-  uint16_t *h, *l;
+  uint16_t* p;
   int ld;
-  int64_t stride;
+  int64_t stride;  // 16-bit values between batches (2 * rows * ld)
+
+  // of the hi part of (row, col); the lo part is 32 further
+  __device__ __forceinline__ int64_t at(int batch, int64_t row, int col) const {
+    return batch * stride + row * (2 * ld) + (col >> 5) * 64 + (col & 31);
+  }
 };
 struct Pair8 {
   u32x4 h, l;
 };
+__device__ __forceinline__ void store_pair(const Split& m, int batch, int64_t row, int col, const float (&v)[8]) {
+  u32x4 h, l;
+  split8(v, h, l);
+  uint16_t* q = m.p + m.at(batch, row, col);
+  *reinterpret_cast<u32x4*>(q) = h;
+  *reinterpret_cast<u32x4*>(q + 32) = l;
+}
 __device__ __forceinline__ Pair8 load_pair(const Split& m, int batch, int row, int col) {
-  const int64_t o = batch * m.stride + static_cast<int64_t>(row) * m.ld + col;
-  return Pair8{*reinterpret_cast<const u32x4*>(m.h + o), *reinterpret_cast<const u32x4*>(m.l + o)};
+  const uint16_t* q = m.p + m.at(batch, row, col);
+  return Pair8{*reinterpret_cast<const u32x4*>(q), *reinterpret_cast<const u32x4*>(q + 32)};
 }
 
 // alpha * C + beta * acc, split, as the output (its rows' padding, where both terms are zero, included);
@@ -77,39 +90,32 @@ __device__ __forceinline__ Pair8 load_pair(const Split& m, int batch, int row, i
 // others get the transposed values
 template <bool kSym>
 struct EpiSplit {
-  static constexpr bool kMirror = kSym;
+  static constexpr bool kMirror = kSym, kAhead = true;
   using Pre = Pair8;
-  Split c;  // C term; c.h null: none
+  Split c;  // C term; c.p null: none
   float alpha, beta;
   Split o;
 
   __device__ __forceinline__ Pre load(const NtArgs& g, int batch, int row, int col) const {
     Pre p = {};
-    if (c.h != nullptr && row < g.M && col < c.ld) p = load_pair(c, batch, row, col);
+    if (c.p != nullptr && row < g.M && col < c.ld) p = load_pair(c, batch, row, col);
     return p;
-  }
-  __device__ __forceinline__ void put(int batch, int row, int col, const float (&v)[8]) const {
-    const int64_t at = batch * o.stride + static_cast<int64_t>(row) * o.ld + col;
-    u32x4 h, l;
-    split8(v, h, l);
-    *reinterpret_cast<u32x4*>(o.h + at) = h;
-    *reinterpret_cast<u32x4*>(o.l + at) = l;
   }
   __device__ __forceinline__ void store(const NtArgs& g, int batch, int row, int col, float (&v)[8], const Pre& p) const {
     float t[8];
     join8(p.h, p.l, t);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(alpha, t[e], beta * v[e]);
-    if (row < g.M && col < o.ld) put(batch, row, col, v);
+    if (row < g.M && col < o.ld) store_pair(o, batch, row, col, v);
   }
   __device__ __forceinline__ void store_t(const NtArgs& g, int batch, int col, int row, const float (&v)[8]) const {
-    if (col < g.N && row < o.ld) put(batch, col, row, v);
+    if (col < g.N && row < o.ld) store_pair(o, batch, col, row, v);
   }
 };
 
 // the last update: o = (alpha * X + beta * acc) 2^-13, stored as the result or applied to the weights
 struct EpiLast {
-  static constexpr bool kMirror = false;
+  static constexpr bool kMirror = false, kAhead = false;
   struct Pre {
     Pair8 x;
     u32x4 w0, w1;
@@ -289,21 +295,17 @@ __global__ __launch_bounds__(256) void first_split_kernel(const Source s, int64_
       // the padding stays zero even where the norm is not finite
       v[e] = col + e < cols ? static_cast<float>(static_cast<double>(u) * inv) * kSplitScale : 0.0f;
     }
-    u32x4 h, l;
-    split8(v, h, l);
-    const int64_t to = batch * o.stride + row * o.ld + col;
-    *reinterpret_cast<u32x4*>(o.h + to) = h;
-    *reinterpret_cast<u32x4*>(o.l + to) = l;
+    store_pair(o, batch, row, col, v);
   }
 }
 
 // ------------------------------------------------------------------------- the products
 template <bool AT, bool BT>
-using Big = NtCfg<256, 256, 128, 64, 2, 2, true, AT, BT, 2>;
+using Big = NtCfg<256, 256, 128, 64, 2, 2, true, AT, BT>;
 template <bool AT, bool BT>
-using Mid = NtCfg<128, 128, 64, 64, 2, 2, true, AT, BT, 2>;
+using Mid = NtCfg<128, 128, 64, 64, 2, 2, true, AT, BT>;
 template <bool AT, bool BT>
-using Small = NtCfg<64, 64, 32, 32, 2, 2, true, AT, BT, 3, true>;
+using Small = NtCfg<64, 64, 32, 32, 2, 2, true, AT, BT, true>;
 
 struct NsPlan {
   int kind;  // 0 Big, 1 Mid, 2 Small
@@ -313,13 +315,13 @@ struct NsPlan {
 // Tile size by how many tiles there are: the largest one that still gives most compute units work.
 NsPlan ns_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri) {
   NsPlan r;
-  r.p = nt_plan(batch, M, N, K, tri, 256, 256, kNtCus);
+  r.p = nt_plan(batch, M, N, K, tri, 256, 256, 32, kNtCus);
   r.kind = 0;
   if (batch * r.p.per_batch >= 96) return r;
-  r.p = nt_plan(batch, M, N, K, tri, 128, 128, 2 * kNtCus);
+  r.p = nt_plan(batch, M, N, K, tri, 128, 128, 32, 2 * kNtCus);
   r.kind = 1;
   if (batch * r.p.per_batch >= 128) return r;
-  r.p = nt_plan(batch, M, N, K, tri, 64, 64, 3 * kNtCus);
+  r.p = nt_plan(batch, M, N, K, tri, 64, 64, 32, 4 * kNtCus);
   r.kind = 2;
   return r;
 }
@@ -336,8 +338,7 @@ struct NsLayout {
   int64_t n, np, ld;    // the smaller side, padded; X's row length (cols, padded)
   NsPlan gram, poly, upd;
   int parts;
-  size_t sums, x0, x1, aa, bb, part, total;  // byte offsets (each matrix hi then lo), end
-  size_t x_bytes, n_bytes;                   // bytes of one part
+  size_t sums, x0, x1, aa, bb, part, total;  // byte offsets, end
 };
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -353,8 +354,7 @@ NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
   l.upd = ns_plan(batch, rows, cols, l.np, false);
   const int64_t parts = (rows * cols + kPerPart - 1) / kPerPart;
   l.parts = static_cast<int>(parts < kPartMax ? parts : kPartMax);
-  l.x_bytes = up256(size_t(2) * batch * rows * l.ld);
-  l.n_bytes = up256(size_t(2) * batch * l.n * l.np);
+  const size_t x_bytes = size_t(4) * batch * rows * l.ld, n_bytes = size_t(4) * batch * l.n * l.np;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -362,10 +362,10 @@ NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
     return at;
   };
   l.sums = take(sizeof(double) * batch * l.parts);
-  l.x0 = take(2 * l.x_bytes);
-  l.x1 = take(2 * l.x_bytes);
-  l.aa = take(2 * l.n_bytes);
-  l.bb = take(2 * l.n_bytes);
+  l.x0 = take(x_bytes);
+  l.x1 = take(x_bytes);
+  l.aa = take(n_bytes);
+  l.bb = take(n_bytes);
   size_t most = 0;
   for (const NsPlan* p : {&l.gram, &l.poly, &l.upd}) most = p->p.ws > most ? p->p.ws : most;
   l.part = take(most);
@@ -432,12 +432,11 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
   const NsLayout l = ns_layout(batch, rows, cols);
   uint8_t* base = static_cast<uint8_t*>(ws);
   double* sums = reinterpret_cast<double*>(base + l.sums);
-  auto split = [&](size_t off, size_t bytes, int64_t ld, int64_t stride) {
-    return Split{reinterpret_cast<uint16_t*>(base + off), reinterpret_cast<uint16_t*>(base + off + bytes),
-                 static_cast<int>(ld), stride};
+  auto split = [&](size_t off, int64_t m_rows, int64_t ld) {
+    return Split{reinterpret_cast<uint16_t*>(base + off), static_cast<int>(ld), 2 * m_rows * ld};
   };
-  Split x[2] = {split(l.x0, l.x_bytes, l.ld, rows * l.ld), split(l.x1, l.x_bytes, l.ld, rows * l.ld)};
-  const Split A = split(l.aa, l.n_bytes, l.np, l.n * l.np), B = split(l.bb, l.n_bytes, l.np, l.n * l.np);
+  const Split x[2] = {split(l.x0, rows, l.ld), split(l.x1, rows, l.ld)};
+  const Split A = split(l.aa, l.n, l.np), B = split(l.bb, l.n, l.np);
   void* part = base + l.part;
   const int n = static_cast<int>(l.n), np = static_cast<int>(l.np);
 
@@ -453,11 +452,10 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
                      dim3(256), 0, s, src, rows, static_cast<int>(cols), l.parts, vec ? 1 : 0, sums, eps, x[0]);
   rc = w4q_launch_status();
 
-  auto operand = [](const Split& m, const uint16_t* (&parts)[2], int64_t& stride, int& ld) {
-    parts[0] = m.h;
-    parts[1] = m.l;
+  auto operand = [](const Split& m, const uint16_t*& p, int64_t& stride, int& ld) {
+    p = m.p;
     stride = m.stride;
-    ld = m.ld;
+    ld = 2 * m.ld;
   };
   int cur = 0;
   for (int i = 0; i < steps && rc == W4Q_OK; ++i, cur ^= 1) {

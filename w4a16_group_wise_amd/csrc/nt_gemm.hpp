@@ -3,31 +3,34 @@
 //
 //   C[b][i][j] = sum_k A[b](i, k) * B[b](j, k)
 //
-// An operand is one 16-bit matrix (bf16, or fp16) or two fp16 matrices hi + lo that hold a value in
-// 22 bits: v = hi + lo with hi = RNE(v), lo = RNE(v - hi).  Products of the parts:
-//   1 x 1 parts: hi hi;   2 x 1: hi hi + lo hi;   2 x 2: hi lo + hi hi + lo hi
+// An operand is one 16-bit matrix (bf16, or fp16) or a split one: two fp16 parts hi + lo that hold a
+// value in 22 bits, v = hi + lo with hi = RNE(v), lo = RNE(v - hi), stored with the parts of each 32
+// columns side by side ([row][column / 32][hi, lo][column % 32]).  Products of the parts:
+//   1 x 1: hi hi;   2 x 1: hi hi + lo hi;   2 x 2: hi lo + hi hi + lo hi
 // (lo lo is below 2^-22 of the product; only the small tile adds it, where products are cheap and few
 // terms average the difference out), each exact in fp32 and summed in fp32 by the matrix cores.
 // What becomes of C is the epilogue's (a functor), so that no C is stored and read again.
 //
 // An operand lies in memory with k along its rows ("along": A[i][k], K a multiple of 32) or across
 // them ("across": A[k][i], any K).  Either is copied to LDS as it lies, by buffer loads straight to
-// LDS, 32 k a stage: along, 64-byte rows with 16-byte chunk c of row r at c ^ nt_swz(r), read in
-// 16-byte fragments; across, rows of the tile's width with chunk c of row k at c ^ nt_tswz(k), read by
-// the transposing LDS read.  Both patterns touch every bank slot once per pass.  So no operand is
-// ever transposed in memory: of the gradients and of X X^T, B X and X^T X each product reads its
-// operands as their producers wrote them.
+// LDS: along, 128 bytes of a row a stage (64 k, or 32 k of both parts: whole cache lines; with 64-byte
+// pieces the L2 served twice the requests), 16-byte chunk c of row r at c ^ nt_swz(r), read in 16-byte
+// fragments; across, rows of the tile's width with chunk c of row k at c ^ nt_tswz(k), read by the
+// transposing LDS read.  Both patterns touch every bank slot once per pass.  So no operand is ever
+// transposed in memory: of the gradients and of X X^T, B X and X^T X each product reads its operands
+// as their producers wrote them.
 //
 // Mapping: BM x BN output tiles, wavefronts of WM x WN (32x32 blocks of v_mfma_f32_32x32x16).
-// NBUF stage buffers; the loads run NBUF - 1 stages ahead, and one barrier per stage both
-// publishes a stage's tiles and frees the buffer of the stage before it.  Rows and k past an
-// operand's end read as zeros (the buffer's bounds); columns past the end of an "across" row read on
-// into the next row and only feed outputs that are never stored.  With three or more buffers the first
-// half of the next stage's fragments is read before the barrier, between the products of the second.
+// Two stage buffers and one barrier per stage, before the stage's last step of 16 k: there every
+// wavefront holds the last fragments of the stage in registers and the next stage has landed, so after
+// it the loads of the stage after next go into the buffer just read (they have a whole stage to
+// land) and the first fragments of the next stage are read between the products of the last step.
+// Rows and k past an operand's end read as zeros (the buffer's bounds); columns past the end of an
+// "across" row read on into the next row and only feed outputs that are never stored.
 //
 // Epilogue: a wavefront passes 32 rows x WN columns at a time through its share of the (then idle)
 // LDS and hands the functor 8 consecutive columns of a row per lane, so that everything the epilogue
-// reads and writes moves in 16-byte pieces; what it reads is loaded one strip ahead.
+// reads and writes moves in 16-byte pieces; what it reads is loaded ahead.
 //
 // Work split: the (tile, stage) iterations of all tiles lie on one line, cut into nblk equal
 // ranges, one per workgroup.  A range that covers a whole tile ends in the epilogue; partial tiles
@@ -43,23 +46,25 @@ namespace w4q {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// position of 16-byte chunk c in 64-byte row r: see gemm.hip for the LDS passes this suits
-__device__ __forceinline__ int nt_swz(int r) { return (((r >> 1) ^ (r >> 4)) & 1) | ((r >> 1) & 2); }
-// position mask of a chunk of k row t, for rows of `width` values: a transposing read of 16 lanes
+// position mask of a chunk of row r in an "along" tile (128-byte rows, 8 chunks).  A 16-byte LDS read
+// is served in passes of 16 lanes: of each half of the wavefront, the four lane quads whose index has
+// even parity, then the other four.  Rows of such a pass differ in (row / 2) % 8 or in parity, so
+// with this mask they hit the 16 distinct slots of 256 bytes.
+__device__ __forceinline__ int nt_swz(int r) { return (r >> 1) & 7; }
+// position mask of a chunk of k row t, for rows of `bytes` bytes: a transposing read of 16 lanes
 // covers 4 consecutive k x 2 chunks and one of 32 lanes 4 k x 4 chunks, which these masks spread over
 // distinct slots modulo 128 and 256 bytes
-template <int width>
+template <int bytes>
 __device__ __forceinline__ int nt_tswz(int t) {
-  return width == 64 ? 2 * (t & 3) : (0xCA60 >> (4 * (t & 3))) & 15;
+  return bytes == 128 ? 2 * (t & 3) : (0xCA60 >> (4 * (t & 3))) & 15;
 }
 
 struct NtArgs {
-  const uint16_t* a[2];
-  const uint16_t* b[2];
-  int64_t sa, sb;     // elements between the batches of A and B
+  const uint16_t *a, *b;
+  int64_t sa, sb;     // 16-bit values between the batches of A and B
   int M, N, K;        // K a multiple of 32 unless both operands lie across
   int ka, kb;         // k rows that A, B really have, where they lie across (K up to the next 32 is zero)
-  int lda, ldb;       // elements per row, multiples of 8
+  int lda, ldb;       // 16-bit values per row (both parts of a split operand), multiples of 8
   int tm, tn;         // tiles along M and N
   int tri;            // 1: M == N and only tiles with row tile >= column tile
   int per_batch;      // tiles of one batch
@@ -89,24 +94,65 @@ __device__ __forceinline__ void nt_tile(const NtArgs& g, int t, int& batch, int&
   }
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int PA_, int PB_, bool F16_, bool AT_, bool BT_, int NBUF_,
-          bool LOLO_ = false>
+// An operand's tile in LDS: W rows (along) or columns (across), P parts, BK k a stage
+template <int W, int P, bool kAcross, int BK, int kWaves>
+struct NtOperand {
+  static constexpr int kRow = kAcross ? 2 * W * P : 128;          // bytes of a row
+  static constexpr int kBytes = kAcross ? BK * kRow : W * kRow;
+  static constexpr int kLoads = kBytes / 1024 / kWaves;           // 1 KB loads per wave
+  static_assert(kAcross || BK * P == 64, "128 bytes of a row a stage");
+  static_assert(kLoads == 1 || kLoads == 2 || kLoads == 4, "loads per wave");
+
+  // byte offset in memory of what lane `lane` brings with load u
+  static __device__ __forceinline__ int load_off(int u, int lane, int ld) {
+    constexpr int kChunks = kRow / 16, kRows = 64 / kChunks;  // chunks of a row, rows of a load
+    const int r = u * kRows + lane / kChunks;
+    const int c = (lane % kChunks) ^ (kAcross ? nt_tswz<kRow>(r) : nt_swz(r));
+    return r * ld * 2 + 16 * c;
+  }
+  // byte offset in the tile of this lane's fragment of rows r0 .. r0 + 31, first step, first part
+  static __device__ __forceinline__ int read_off(int r0, int lane) {
+    if constexpr (kAcross) {
+      // 16-lane group rg, lane rj in it: k 8 (rg / 2) + rj / 4 (+ 4 in the second read), values
+      // 16 (rg % 2) + 4 (rj % 4); it receives value 16 (rg % 2) + rj of four consecutive k
+      const int rg = lane >> 4, rj = lane & 15;
+      const int t = 8 * (rg >> 1) + (rj >> 2);
+      const int c = r0 / 8 * P + 2 * (rg & 1) + ((rj >> 1) & 1);
+      return t * kRow + 16 * (c ^ nt_tswz<kRow>(t)) + 8 * (rj & 1);
+    } else {
+      const int r = r0 + (lane & 31);
+      return r * 128 + 16 * ((lane >> 5) ^ nt_swz(r));
+    }
+  }
+  static __device__ __forceinline__ u32x4 read(const uint8_t* tile, int off, int kk, int part) {
+    if constexpr (kAcross) {
+      const uint8_t* p = tile + (off ^ (64 * part)) + kk * 16 * kRow;
+      const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(p));
+      const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(p + 4 * kRow));
+      return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *reinterpret_cast<const u32x4*>(tile + (off ^ (32 * kk + 64 * part)));
+    }
+  }
+};
+
+template <int BM_, int BN_, int WM_, int WN_, int PA_, int PB_, bool F16_, bool AT_, bool BT_, bool LOLO_ = false>
 struct NtCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PA = PA_, PB = PB_, NBUF = NBUF_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PA = PA_, PB = PB_;
   static constexpr bool F16 = F16_, AT = AT_, BT = BT_, LOLO = LOLO_;  // AT, BT: operand lies across
+  static constexpr int BK = PA == 1 && PB == 1 ? 64 : 32, KS = BK / 16;  // k and steps of a stage
   static constexpr int kWavesM = BM / WM, kWavesN = BN / WN, kWaves = kWavesM * kWavesN;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int MB = WM / 32, NB = WN / 32;
-  static constexpr int LA = BM / 16 / kWaves, LB = BN / 16 / kWaves;  // 1 KB loads per wave and part
-  static constexpr int kOps = PA * LA + PB * LB;                      // loads per wave and stage
-  static constexpr int kBytesA = BM * 64, kBytesB = BN * 64;
-  static constexpr int kStage = PA * kBytesA + PB * kBytesB;
-  static constexpr int kLds = NBUF * kStage;
+  using OpA = NtOperand<BM, PA, AT, BK, kWaves>;
+  using OpB = NtOperand<BN, PB, BT, BK, kWaves>;
+  static constexpr int kOps = OpA::kLoads + OpB::kLoads;              // loads per wave and stage
+  static constexpr int kStage = OpA::kBytes + OpB::kBytes;
+  static constexpr int kLds = 2 * kStage;
   static constexpr int kTileElems = BM * BN;
   static constexpr int kPitch = WN + 4;                               // floats per row of an epilogue strip
   static constexpr int kReads = PA * MB * (AT ? 2 : 1) + PB * NB * (BT ? 2 : 1);  // LDS reads per step
   static constexpr int kMma = MB * NB * (PA + PB - 1 + (LOLO ? 1 : 0));           // products per step
-  static_assert(LA >= 1 && LB >= 1 && LA <= 2 && LB <= 2, "1 or 2 loads per wave and part");
   static_assert(kLds <= 160 * 1024 && kLds / kWaves >= 32 * kPitch * 4, "LDS");
   static_assert(!LOLO || (PA == 2 && PB == 2), "parts");
 };
@@ -119,8 +165,6 @@ __device__ __forceinline__ f32x16 nt_mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-#define W4Q_TR_LDS(p) ((__attribute__((address_space(3))) v4i16*)(p))
-
 // partial-tile layout: wavefront, block, 16-byte quarter, lane (1 KB per store instruction)
 template <class C>
 __device__ __forceinline__ int64_t nt_part_off(int w, int blk, int q, int lane) {
@@ -130,7 +174,8 @@ __device__ __forceinline__ int64_t nt_part_off(int w, int blk, int q, int lane) 
 // ---------------------------------------------------------------------------- epilogue strips
 // A strip is 32 rows x WN columns of a wavefront's tile.  Lane l takes 8 columns from 8 (l % (WN / 8)) of
 // rows l / (WN / 8) + kRows i.  The functor gives, for 8 columns of one row:
-//   Pre load(g, batch, row, col)                     what the epilogue reads there
+//   Pre load(g, batch, row, col)                     what the epilogue reads there (kAhead: one strip
+//                                                    ahead of its use, in twice the registers)
 //   void store(g, batch, row, col, v[8], pre)        writes the outputs; leaves in v what a mirrored
 //                                                    store shall write
 //   kMirror, void store_t(g, batch, col, row, v[8])  symmetric results: 8 rows of one column
@@ -190,10 +235,21 @@ __device__ __forceinline__ void nt_strip_store(const NtArgs& g, const Epi& epi, 
   asm volatile("" ::: "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void nt_dma(uint32_t lds, v4i32 rs, const int (&vo)[N]) {
+  if constexpr (N == 4)
+    dma_x4(lds, rs, vo);
+  else if constexpr (N == 2)
+    dma_x2(lds, rs, vo[0], vo[1]);
+  else
+    dma_x1(lds, rs, vo[0]);
+}
+
 template <class C, class Epi>
 __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const Epi epi) {
+  using OpA = typename C::OpA;
+  using OpB = typename C::OpB;
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
-  constexpr int D = C::NBUF - 1;  // stages the loads run ahead
   const int lb = static_cast<int>(blockIdx.x & 7) * g.per_xcd + static_cast<int>(blockIdx.x >> 3);
   if (lb >= g.nblk) return;
   const int it_begin = lb * g.chunk;
@@ -205,57 +261,15 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
   const int wm = wid / C::kWavesN, wn = wid % C::kWavesN;
   const uint32_t lds0 = lds_addr(lds);
 
-  // byte offsets of this lane's loads of a stage: load u of a part fills 1 KB of the part's tile
-  auto load_off = [&](int u, int ld, auto across, auto width) {
-    if constexpr (decltype(across)::value) {
-      constexpr int W = decltype(width)::value, CPR = W / 8, RPL = 64 / CPR;  // chunks per row, rows per load
-      const int t = u * RPL + lane / CPR;
-      return t * ld * 2 + 16 * ((lane % CPR) ^ nt_tswz<W>(t));
-    } else {
-      const int r = 16 * u + (lane >> 2);
-      return r * ld * 2 + 16 * ((lane & 3) ^ nt_swz(r));
-    }
-  };
-  int avo[C::LA], bvo[C::LB];
+  int avo[OpA::kLoads], bvo[OpB::kLoads], aro[C::MB], bro[C::NB];
 #pragma unroll
-  for (int q = 0; q < C::LA; ++q)
-    avo[q] = load_off(wid * C::LA + q, g.lda, std::bool_constant<C::AT>{}, std::integral_constant<int, C::BM>{});
+  for (int q = 0; q < OpA::kLoads; ++q) avo[q] = OpA::load_off(wid * OpA::kLoads + q, lane, g.lda);
 #pragma unroll
-  for (int q = 0; q < C::LB; ++q)
-    bvo[q] = load_off(wid * C::LB + q, g.ldb, std::bool_constant<C::BT>{}, std::integral_constant<int, C::BN>{});
-  // byte offsets of this lane's fragments within a part's tile, first step of 16 k
-  auto read_off = [&](int r0, auto across, auto width) {
-    if constexpr (decltype(across)::value) {
-      constexpr int W = decltype(width)::value;
-      // 16-lane group rg, lane rj in it: k 8 (rg / 2) + rj / 4 (+ 4 in the second read), values
-      // 16 (rg % 2) + 4 (rj % 4); it receives value 16 (rg % 2) + rj of four consecutive k
-      const int rg = lane >> 4, rj = lane & 15;
-      const int t = 8 * (rg >> 1) + (rj >> 2);
-      const int c = r0 / 8 + 2 * (rg & 1) + ((rj >> 1) & 1);
-      return t * (2 * W) + 16 * (c ^ nt_tswz<W>(t)) + 8 * (rj & 1);
-    } else {
-      const int r = r0 + (lane & 31);
-      return r * 64 + 16 * ((lane >> 5) ^ nt_swz(r));
-    }
-  };
-  int aro[C::MB], bro[C::NB];
+  for (int q = 0; q < OpB::kLoads; ++q) bvo[q] = OpB::load_off(wid * OpB::kLoads + q, lane, g.ldb);
 #pragma unroll
-  for (int i = 0; i < C::MB; ++i)
-    aro[i] = read_off(wm * C::WM + 32 * i, std::bool_constant<C::AT>{}, std::integral_constant<int, C::BM>{});
+  for (int i = 0; i < C::MB; ++i) aro[i] = OpA::read_off(wm * C::WM + 32 * i, lane);
 #pragma unroll
-  for (int j = 0; j < C::NB; ++j)
-    bro[j] = read_off(wn * C::WN + 32 * j, std::bool_constant<C::BT>{}, std::integral_constant<int, C::BN>{});
-  auto read_frag = [&](const uint8_t* tile, int off, int kk, auto across, auto width) -> u32x4 {
-    if constexpr (decltype(across)::value) {
-      constexpr int W = decltype(width)::value;
-      const uint8_t* p = tile + off + kk * 16 * 2 * W;
-      const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(W4Q_TR_LDS(p));
-      const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(W4Q_TR_LDS(p + 4 * 2 * W));
-      return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    } else {
-      return *reinterpret_cast<const u32x4*>(tile + (off ^ (32 * kk)));
-    }
-  };
+  for (int j = 0; j < C::NB; ++j) bro[j] = OpB::read_off(wn * C::WN + 32 * j, lane);
 
   int it = it_begin;
   while (it < it_end) {
@@ -265,41 +279,44 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     int batch, ti, tj;
     nt_tile(g, t, batch, ti, tj);
     const int m0 = ti * C::BM, n0 = tj * C::BN;
-    const uint16_t* abase[2] = {g.a[0] + batch * g.sa, C::PA == 2 ? g.a[1] + batch * g.sa : nullptr};
-    const uint16_t* bbase[2] = {g.b[0] + batch * g.sb, C::PB == 2 ? g.b[1] + batch * g.sb : nullptr};
+    const uint16_t* abase = g.a + batch * g.sa;
+    const uint16_t* bbase = g.b + batch * g.sb;
 
-    // loads of stage s into buffer `buf` (past the range: empty loads, which write zeros)
-    auto issue_part = [&](const uint16_t* base, int s, bool live, int r0, int rows, int ld, uint32_t dst, auto across,
-                          auto width, int krows, const auto& vo) {
-      constexpr int W = decltype(width)::value;
+    // an operand's loads of stage s (past the range: empty loads, which write zeros)
+    auto issue_op = [&](const uint16_t* base, int s, int r0, int rows, int ld, int krows, uint32_t dst, auto op, int width,
+                        int parts, bool across, const auto& vo) {
+      using Op = decltype(op);
+      const bool live = s < s1;
       int64_t off;
       int bytes;
-      if constexpr (decltype(across)::value) {
-        const int left = krows - 32 * s;
-        off = static_cast<int64_t>(32 * s) * ld + r0;
-        bytes = ((left < 32 ? left : 32) * ld - r0) * 2;
+      if (across) {
+        const int left = krows - C::BK * s;
+        off = static_cast<int64_t>(C::BK * s) * ld + r0 * parts;
+        bytes = ((left < C::BK ? left : C::BK) * ld - r0 * parts) * 2;
       } else {
         const int left = rows - r0;
-        off = static_cast<int64_t>(r0) * ld + 32 * s;
-        bytes = ((left < W ? left : W) * ld - 32 * s) * 2;
+        off = static_cast<int64_t>(r0) * ld + 64 * s;
+        bytes = ((left < width ? left : width) * ld - 64 * s) * 2;
       }
       const v4i32 rs = buffer_rsrc(base + (live ? off : 0), live ? bytes : 0);
-      if constexpr (sizeof(vo) == 8)
-        dma_x2(dst + wid * 2048, rs, vo[0], vo[1]);
-      else
-        dma_x1(dst + wid * 1024, rs, vo[0]);
+      const uint32_t to = dst + wid * (Op::kLoads * 1024);
+      if (C::BK == 64 && !across && g.K - 64 * s == 32) {
+        // half a stage: the second 32 k of each row (chunks 4..7) lie beyond K and read as zeros
+        int half[Op::kLoads];
+#pragma unroll
+        for (int q = 0; q < Op::kLoads; ++q) {
+          const int r = 8 * (wid * Op::kLoads + q) + (lane >> 3);
+          half[q] = ((lane ^ nt_swz(r)) & 4) != 0 ? 0x7FFFFFF0 : vo[q];
+        }
+        nt_dma(to, rs, half);
+      } else {
+        nt_dma(to, rs, vo);
+      }
     };
     auto issue = [&](int s, int buf) {
-      const bool live = s < s1;
-      uint32_t dst = lds0 + buf * C::kStage;
-#pragma unroll
-      for (int p = 0; p < C::PA; ++p, dst += C::kBytesA)
-        issue_part(abase[p], s, live, m0, g.M, g.lda, dst, std::bool_constant<C::AT>{},
-                   std::integral_constant<int, C::BM>{}, g.ka, avo);
-#pragma unroll
-      for (int p = 0; p < C::PB; ++p, dst += C::kBytesB)
-        issue_part(bbase[p], s, live, n0, g.N, g.ldb, dst, std::bool_constant<C::BT>{},
-                   std::integral_constant<int, C::BN>{}, g.kb, bvo);
+      const uint32_t dst = lds0 + buf * C::kStage;
+      issue_op(abase, s, m0, g.M, g.lda, g.ka, dst, OpA{}, C::BM, C::PA, C::AT, avo);
+      issue_op(bbase, s, n0, g.N, g.ldb, g.kb, dst + OpA::kBytes, OpB{}, C::BN, C::PB, C::BT, bvo);
     };
 
     f32x16 acc[C::MB][C::NB];
@@ -315,19 +332,15 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     };
     auto load = [&](int buf, int kk, Frags& f) {
       const uint8_t* pa = lds + buf * C::kStage;
-      const uint8_t* pb = pa + C::PA * C::kBytesA;
+      const uint8_t* pb = pa + OpA::kBytes;
 #pragma unroll
       for (int p = C::PB - 1; p >= 0; --p)
 #pragma unroll
-        for (int j = 0; j < C::NB; ++j)
-          f.b[p][j] = read_frag(pb + p * C::kBytesB, bro[j], kk, std::bool_constant<C::BT>{},
-                                std::integral_constant<int, C::BN>{});
+        for (int j = 0; j < C::NB; ++j) f.b[p][j] = OpB::read(pb, bro[j], kk, p);
 #pragma unroll
       for (int p = 0; p < C::PA; ++p)
 #pragma unroll
-        for (int i = 0; i < C::MB; ++i)
-          f.a[p][i] = read_frag(pa + p * C::kBytesA, aro[i], kk, std::bool_constant<C::AT>{},
-                                std::integral_constant<int, C::BM>{});
+        for (int i = 0; i < C::MB; ++i) f.a[p][i] = OpA::read(pa, aro[i], kk, p);
     };
     auto mma_parts = [&](const u32x4 (&a)[C::MB], const u32x4 (&b)[C::NB]) {
 #pragma unroll
@@ -363,37 +376,25 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
     };
-    auto next = [](int buf, int n) { return buf + n >= C::NBUF ? buf + n - C::NBUF : buf + n; };
-
     Frags f0, f1;
-#pragma unroll
-    for (int d = 0; d < D; ++d) issue(s0 + d, d);
+    issue(s0, 0);
+    issue(s0 + 1, 1);
+    sync(std::integral_constant<int, C::kOps>{});  // stage s0 has landed
+    load(0, 0, f0);
     int buf = 0;
-    if constexpr (D >= 2) {
-      sync(std::integral_constant<int, (D - 1) * C::kOps>{});  // stage s0
-      load(0, 0, f0);
-      for (int s = s0; s < s1; ++s) {
-        // stages s and s + 1 have landed; the buffer of s - 1 is free
-        sync(std::integral_constant<int, (D - 2) * C::kOps>{});
-        issue(s + D, next(buf, D));
-        load(buf, 1, f1);
-        mma(f0);
-        pattern();
-        buf = next(buf, 1);
-        load(buf, 0, f0);  // (past the range: a buffer of zeros, never used)
-        mma(f1);
+    for (int s = s0; s < s1; ++s) {
+#pragma unroll
+      for (int kk = 0; kk + 1 < C::KS; ++kk) {
+        load(buf, kk + 1, (kk & 1) != 0 ? f0 : f1);
+        mma((kk & 1) != 0 ? f1 : f0);
         pattern();
       }
-    } else {
-      for (int s = s0; s < s1; ++s) {
-        sync(std::integral_constant<int, 0>{});  // stage s has landed; the other buffer is free
-        issue(s + 1, buf ^ 1);
-        load(buf, 0, f0);
-        load(buf, 1, f1);
-        mma(f0);
-        mma(f1);
-        buf ^= 1;
-      }
+      sync(std::integral_constant<int, 0>{});  // stage s + 1 has landed; nobody reads buffer `buf` any more
+      issue(s + 2, buf);
+      buf ^= 1;
+      load(buf, 0, f0);  // (past the range: a buffer of zeros, never used)
+      mma(f1);
+      pattern();
     }
     // nothing is in flight or still being read when the buffers are used for other things
     sync(std::integral_constant<int, 0>{});
@@ -401,12 +402,14 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     if (s0 == 0 && s1 == g.S) {
       float* strip = reinterpret_cast<float*>(lds + wid * (C::kLds / C::kWaves));
       const int row0 = m0 + wm * C::WM, col0 = n0 + wn * C::WN;
-      typename Epi::Pre pre[2][NtStrip<C>::kPasses];
+      constexpr int kSets = Epi::kAhead ? 2 : 1;
+      typename Epi::Pre pre[kSets][NtStrip<C>::kPasses];
       nt_strip_load<C>(g, epi, batch, row0, col0, lane, pre[0]);
 #pragma unroll
       for (int i = 0; i < C::MB; ++i) {
-        if (i + 1 < C::MB) nt_strip_load<C>(g, epi, batch, row0 + 32 * (i + 1), col0, lane, pre[(i + 1) & 1]);
-        nt_strip_store<C>(g, epi, batch, row0 + 32 * i, col0, ti == tj, acc[i], lane, strip, pre[i & 1]);
+        if (kSets == 2 && i + 1 < C::MB) nt_strip_load<C>(g, epi, batch, row0 + 32 * (i + 1), col0, lane, pre[(i + 1) % kSets]);
+        nt_strip_store<C>(g, epi, batch, row0 + 32 * i, col0, ti == tj, acc[i], lane, strip, pre[i % kSets]);
+        if (kSets == 1 && i + 1 < C::MB) nt_strip_load<C>(g, epi, batch, row0 + 32 * (i + 1), col0, lane, pre[0]);
       }
       if (it + (s1 - s0) < it_end) sync(std::integral_constant<int, 0>{});  // the next tile's loads reuse the LDS
     } else {
@@ -468,7 +471,7 @@ __global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi 
 
 // ------------------------------------------------------------------------------ host side
 constexpr int kNtCus = 256;
-constexpr int kNtMinChunk = 16;  // stages a range covers at least
+constexpr int kNtMinK = 512;  // k a range covers at least
 
 struct NtPlan {
   int64_t tm, tn, per_batch, S, total, chunk, nblk;
@@ -478,19 +481,19 @@ struct NtPlan {
 // The split of `batch` products of M x N x K on BM x BN tiles where `slots` workgroups run at once:
 // one tile per workgroup when the tiles fill (nearly) whole rounds of the device, else equal
 // ranges of stages, one per slot.
-inline NtPlan nt_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, int BM, int BN, int slots) {
+inline NtPlan nt_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, int BM, int BN, int BK, int slots) {
   NtPlan p;
   p.tm = (M + BM - 1) / BM;
   p.tn = (N + BN - 1) / BN;
   p.per_batch = tri ? p.tm * (p.tm + 1) / 2 : p.tm * p.tn;
-  p.S = (K + 31) / 32;
+  p.S = (K + BK - 1) / BK;
   const int64_t tiles = batch * p.per_batch;
   p.total = tiles * p.S;
   p.chunk = p.S;
   const int64_t rounds = (tiles + slots - 1) / slots;
   if (tiles * 100 < rounds * slots * 85 && rounds <= 4) {
     int64_t chunk = (p.total + slots - 1) / slots;
-    if (chunk < kNtMinChunk) chunk = kNtMinChunk;
+    if (chunk < kNtMinK / BK) chunk = kNtMinK / BK;
     if (chunk < p.S || (rounds > 1 && chunk < p.S * rounds)) p.chunk = chunk;
   }
   p.nblk = (p.total + p.chunk - 1) / p.chunk;
