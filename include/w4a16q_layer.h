@@ -83,12 +83,17 @@ int lsq_linear_bwd_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int gr
  * 1: weights rounded to bf16) with the forward's epilogue applied to the fp32 sums:
  *   y[m][n] = act(sum_k x[m][k] * w_hat[n][k] + bias[n]) + residual[m][n]
  *   bias fp32 [d_out] or NULL; residual [m][d_out] of y's type or NULL (may be y itself); the other
- *   arguments, limits and the workspace (w4a16_gemm_workspace_size, w4a16_gemm_dq_workspace_size)
- *   as for those calls, and with one row d_out < 2^31 and d_in <= 2^24 (W4Q_EUNSUPPORTED).
+ *   arguments and limits as for those calls, and with one row d_out < 2^31 and d_in <= 2^24
+ *   (W4Q_EUNSUPPORTED).
+ *   workspace  NULL with 0 bytes, or 256-B aligned scratch.  With the size the query returns the fastest
+ *   schedule runs (for many rows with w_mode 1 that holds the weights dequantised once); with
+ *   less, one whose scratch fits, with the same arithmetic up to the order of the sums.
  */
 int w4a16_linear(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* scale_f16,
                  int64_t d_out, int64_t d_in, const float* bias, int act, const void* residual, void* y,
                  int y_dtype, int w_mode, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+int w4a16_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int w_mode, size_t* bytes);
 
 /*
  * newton_schulz -- an update orthogonalised by Newton-Schulz products (the published Muon

@@ -81,6 +81,7 @@ LAYER_SIGNATURES = {
     "lsq_linear_bwd": (_INT, [_P, _I64, _P, _I64, _I64, _P, _INT, _INT, _P, _P, _P, _P, _P, _SZ, _P]),
     "lsq_linear_bwd_workspace_size": (_INT, [_I64, _I64, _I64, _INT, _INT, _P]),
     "w4a16_linear": (_INT, [_P, _I64, _P, _P, _I64, _I64, _P, _INT, _P, _P, _INT, _INT, _P, _SZ, _P]),
+    "w4a16_linear_workspace_size": (_INT, [_I64, _I64, _I64, _INT, _P]),
     "newton_schulz": (_INT, [_P, _INT, _I64, _I64, _I64, _INT, _P, ctypes.c_double, _P, _INT, _P, _SZ, _P]),
     "newton_schulz_workspace_size": (_INT, [_I64, _I64, _I64, _P]),
     "muon_step": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P]),

@@ -101,6 +101,15 @@ int lsq_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t 
                                grad_bias, workspace, stream);
 }
 
+int w4a16_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int w_mode, size_t* bytes) {
+  if (!bytes || !dtype_ok(w_mode)) return W4Q_EINVAL;
+  const int rc = check_layer(m, d_out, d_in);
+  if (rc != W4Q_OK) return rc;
+  const size_t dq = w_mode == 1 ? w4q_linear_dq_workspace(m, d_out, d_in) : 0;
+  *bytes = dq != 0 ? dq : w4q_gemm_workspace(m, d_out, d_in, w_mode);
+  return W4Q_OK;
+}
+
 int w4a16_linear(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* scale_f16,
                  int64_t d_out, int64_t d_in, const float* bias, int act, const void* residual, void* y,
                  int y_dtype, int w_mode, void* workspace, size_t workspace_bytes, hipStream_t stream) {
@@ -114,6 +123,9 @@ int w4a16_linear(const uint16_t* x, int64_t m, const uint8_t* packed, const uint
   const w4q::W4Epilogue ep = {bias, residual, act};
   if (w_mode == 0 && m <= 16)
     return w4q_launch_gemv(x, m, packed, scale_f16, d_out, d_in, y, y_dtype, stream, &ep);
+  const size_t dq = w_mode == 1 ? w4q_linear_dq_workspace(m, d_out, d_in) : 0;
+  if (dq != 0 && workspace != nullptr && workspace_bytes >= dq)
+    return w4q_launch_linear_dq(x, m, packed, scale_f16, d_out, d_in, ep, y, y_dtype, workspace, workspace_bytes, stream);
   return w4q_launch_gemm(x, m, packed, scale_f16, d_out, d_in, y, y_dtype, w_mode, workspace, workspace_bytes, stream,
                          &ep);
 }

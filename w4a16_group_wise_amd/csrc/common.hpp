@@ -89,6 +89,9 @@ constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) 
 // the same, also waiting for every LDS operation of this wavefront
 constexpr int waitcnt_vm_lgkm0(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
 
+// s_waitcnt immediate that waits for this wavefront's LDS operations only
+constexpr int waitcnt_lgkm0() { return 15 | (3 << 14) | (7 << 4); }
+
 // LDS byte address of a __shared__ object
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
@@ -229,6 +232,10 @@ size_t w4q_linear_bwd_workspace(int64_t m, int64_t d_out, int64_t d_in, int dy_f
 int w4q_launch_linear_fwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,
                           const float* bias, int act, const void* res, uint16_t* z, void* y, int y_dtype,
                           void* ws, size_t ws_bytes, hipStream_t s);
+size_t w4q_linear_dq_workspace(int64_t m, int64_t d_out, int64_t d_in);
+int w4q_launch_linear_dq(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16, int64_t d_out,
+                         int64_t d_in, const w4q::W4Epilogue& ep, void* y, int y_dtype, void* ws, size_t ws_bytes,
+                         hipStream_t s);
 int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,
                           const void* dy, int dy_f32, int act, const uint16_t* z, uint16_t* dx, float* dw,
                           float* db, void* ws, hipStream_t s);

@@ -32,7 +32,8 @@ constexpr float kDactMax = 1.13f; // |act'| <= 1.1290 (gelu), 1.0999 (silu), 1 (
 
 // ------------------------------------------------------------------------------ epilogues
 struct EpiLinear {
-  static constexpr bool kMirror = false, kAhead = true;
+  static constexpr bool kMirror = false;
+  static constexpr int kLoads = 0;
   struct Pre {
     u32x4 r0, r1;
   };
@@ -42,50 +43,54 @@ struct EpiLinear {
   int y_dtype;
   int vec;      // 8 columns of a row may be moved in 16-byte pieces
 
+  __device__ __forceinline__ bool whole() const { return vec != 0; }
   __device__ __forceinline__ Pre load(const NtArgs& g, int, int row, int col) const {
     Pre p = {};
     if (ep.res != nullptr && vec && row < g.M && col < g.N) load8(ep.res, static_cast<int64_t>(row) * g.N + col, y_dtype, p.r0, p.r1);
     return p;
   }
-  __device__ __forceinline__ void store(const NtArgs& g, int, int row, int col, float (&v)[8], const Pre& p) const {
-    if (row >= g.M || col >= g.N) return;
-    const int64_t o = static_cast<int64_t>(row) * g.N + col;
-    const int left = g.N - col;
-    if (ep.bias != nullptr) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += ep.bias[e < left ? col + e : col];
-    }
-    if (z != nullptr) {
-      if (vec) {
-        store8(z, o, 1, v);
-      } else {
-        for (int e = 0; e < 8; ++e)
-          if (e < left) z[o + e] = bf16_bits(v[e]);
-      }
-    }
-    float r[8];
-    unpack8(p.r0, p.r1, y_dtype, r);
-    if (ep.res != nullptr && !vec)
-      for (int e = 0; e < 8; ++e)
-        if (e < left)
-          r[e] = y_dtype == 0 ? static_cast<const float*>(ep.res)[o + e] : bf16_val(static_cast<const uint16_t*>(ep.res)[o + e]);
-    // one branch on the activation for all eight values
+  __device__ __forceinline__ void activate(float (&v)[8]) const {  // one branch for all eight values
     switch (ep.act) {
       case W4Q_ACT_RELU: act8<W4Q_ACT_RELU>(v); break;
       case W4Q_ACT_GELU: act8<W4Q_ACT_GELU>(v); break;
       case W4Q_ACT_SILU: act8<W4Q_ACT_SILU>(v); break;
       default: break;
     }
+  }
+  __device__ __forceinline__ void store(const NtArgs& g, int, int row, int col, float (&v)[8], const Pre& p) const {
+    if (row >= g.M || col >= g.N) return;
+    const int64_t o = static_cast<int64_t>(row) * g.N + col;
+    if (ep.bias != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += ep.bias[col + e];
+    }
+    if (z != nullptr) store8(z, o, 1, v);
+    activate(v);
     if (ep.res != nullptr) {
+      float r[8];
+      unpack8(p.r0, p.r1, y_dtype, r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += r[e];
     }
-    if (vec) {
-      store8(y, o, y_dtype, v);
-    } else {
-      for (int e = 0; e < 8; ++e)
-        if (e < left) store1(y, o + e, y_dtype, v[e]);
+    store8(y, o, y_dtype, v);
+  }
+  __device__ __forceinline__ float load1(const NtArgs& g, int, int row, int col) const {
+    if (ep.res == nullptr || row >= g.M || col >= g.N) return 0.0f;
+    const int64_t o = static_cast<int64_t>(row) * g.N + col;
+    return y_dtype == 0 ? static_cast<const float*>(ep.res)[o] : bf16_val(static_cast<const uint16_t*>(ep.res)[o]);
+  }
+  __device__ __forceinline__ void store1(const NtArgs& g, int, int row, int col, float (&v)[8], const float (&r)[8]) const {
+    const int64_t o = static_cast<int64_t>(row) * g.N + col;
+    const float bv = ep.bias != nullptr ? ep.bias[col] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] += bv;
+      if (z != nullptr && row + e < g.M) z[o + static_cast<int64_t>(e) * g.N] = bf16_bits(v[e]);
     }
+    activate(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (row + e < g.M) w4q::store1(y, o + static_cast<int64_t>(e) * g.N, y_dtype, v[e] + r[e]);
   }
   template <int kAct>
   static __device__ __forceinline__ void act8(float (&v)[8]) {
@@ -96,7 +101,8 @@ struct EpiLinear {
 
 // a gradient product: the operands' powers of two taken back, stored as fp32 or bf16
 struct EpiGrad {
-  static constexpr bool kMirror = false, kAhead = true;
+  static constexpr bool kMirror = false;
+  static constexpr int kLoads = 1;
   struct Pre {
     int e;
   };
@@ -105,20 +111,21 @@ struct EpiGrad {
   void* out;
   int out_dtype, vec;
 
-  __device__ __forceinline__ Pre load(const NtArgs&, int, int, int) const {
-    return Pre{e0 != nullptr ? -(*e0 + *e1) : 0};
-  }
+  __device__ __forceinline__ bool whole() const { return vec != 0; }
+  __device__ __forceinline__ int exponent() const { return e0 != nullptr ? -(*e0 + *e1) : 0; }
+  __device__ __forceinline__ Pre load(const NtArgs&, int, int, int) const { return Pre{exponent()}; }
   __device__ __forceinline__ void store(const NtArgs& g, int, int row, int col, float (&v)[8], const Pre& p) const {
     if (row >= g.M || col >= g.N) return;
-    const int64_t o = static_cast<int64_t>(row) * g.N + col;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], p.e);
-    if (vec) {
-      store8(out, o, out_dtype, v);
-    } else {
-      for (int e = 0; e < 8; ++e)
-        if (col + e < g.N) store1(out, o + e, out_dtype, v[e]);
-    }
+    store8(out, static_cast<int64_t>(row) * g.N + col, out_dtype, v);
+  }
+  __device__ __forceinline__ float load1(const NtArgs&, int, int, int) const { return 0.0f; }
+  __device__ __forceinline__ void store1(const NtArgs& g, int, int row, int col, float (&v)[8], const float (&)[8]) const {
+    const int x = exponent();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (row + e < g.M) w4q::store1(out, static_cast<int64_t>(row + e) * g.N + col, out_dtype, __builtin_ldexpf(v[e], x));
   }
 };
 
@@ -227,13 +234,21 @@ struct DzArgs {
   const void* dy;
   int dy_f32;
   const uint16_t* z;
-  int act, vec;
+  int act;
   int64_t m, n, np;
   uint16_t *hi, *both;  // null: not wanted
   float* bsum;        // [ceil(m / 64)][n] or null
   const float* parts;
   int* exp_out;
 };
+// the fp16 parts of v 2^e; an infinite v stays infinite (its rest is NaN)
+__device__ __forceinline__ void dz_split(float v, int e, uint16_t& h, uint16_t& l) {
+  const float s = __builtin_ldexpf(v, e);
+  const _Float16 hi = static_cast<_Float16>(s);
+  const float rest = s - static_cast<float>(hi);
+  h = __builtin_bit_cast(uint16_t, hi);
+  l = rest == rest ? f32_to_f16_bits(rest) : 0;
+}
 template <int kAct>
 __device__ __forceinline__ void dact8(float (&v)[8], const float (&z)[8]) {
 #pragma unroll
@@ -256,27 +271,13 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
     if (row >= a.m || col >= a.np) continue;
     const int64_t o = row * a.n + col;
     float v[8], zv[8];
-    u32x4 raw = {0, 0, 0, 0};  // dy as it lies (bf16)
-    if (a.vec) {
-      u32x4 d0 = {0, 0, 0, 0}, d1 = {0, 0, 0, 0}, z0 = {0, 0, 0, 0};
-      if (col < a.n) {  // n is a multiple of 8
-        load8(a.dy, o, a.dy_f32 ? 0 : 1, d0, d1);
-        if (a.act != W4Q_ACT_NONE) z0 = *reinterpret_cast<const u32x4*>(a.z + o);
-      }
-      unpack8(d0, d1, a.dy_f32 ? 0 : 1, v);
-      unpack8(z0, z0, 1, zv);
-      raw = d0;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool in = col + j < a.n;
-        uint16_t bits = 0;
-        if (in && !a.dy_f32) bits = static_cast<const uint16_t*>(a.dy)[o + j];
-        v[j] = !in ? 0.0f : a.dy_f32 ? static_cast<const float*>(a.dy)[o + j] : bf16_val(bits);
-        zv[j] = in && a.act != W4Q_ACT_NONE ? bf16_val(a.z[o + j]) : 0.0f;
-        raw[j >> 1] |= static_cast<uint32_t>(bits) << (16 * (j & 1));
-      }
+    u32x4 d0 = {0, 0, 0, 0}, d1 = {0, 0, 0, 0}, z0 = {0, 0, 0, 0};
+    if (col < a.n) {  // n is a multiple of 8
+      load8(a.dy, o, a.dy_f32 ? 0 : 1, d0, d1);
+      if (a.act != W4Q_ACT_NONE) z0 = *reinterpret_cast<const u32x4*>(a.z + o);
     }
+    unpack8(d0, d1, a.dy_f32 ? 0 : 1, v);
+    unpack8(z0, z0, 1, zv);
     switch (a.act) {  // (padding columns: 0 times a finite slope)
       case W4Q_ACT_RELU: dact8<W4Q_ACT_RELU>(v, zv); break;
       case W4Q_ACT_GELU: dact8<W4Q_ACT_GELU>(v, zv); break;
@@ -291,17 +292,11 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
       u32x4 h, l;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t hb[2], lb[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float s = __builtin_ldexpf(v[2 * j + q], e);
-          const _Float16 hi = static_cast<_Float16>(s);
-          const float rest = s - static_cast<float>(hi);
-          hb[q] = __builtin_bit_cast(uint16_t, hi);
-          lb[q] = rest == rest ? f32_to_f16_bits(rest) : 0;  // an infinite dz stays infinite (its rest is NaN)
-        }
-        h[j] = hb[0] | (hb[1] << 16);
-        l[j] = lb[0] | (lb[1] << 16);
+        uint16_t h0, l0, h1, l1;
+        dz_split(v[2 * j], e, h0, l0);
+        dz_split(v[2 * j + 1], e, h1, l1);
+        h[j] = h0 | (static_cast<uint32_t>(h1) << 16);
+        l[j] = l0 | (static_cast<uint32_t>(l1) << 16);
       }
       if (a.hi != nullptr) *reinterpret_cast<u32x4*>(a.hi + at) = h;
       if (a.both != nullptr) {  // the split matrix: the parts of 32 columns side by side
@@ -310,7 +305,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
         *reinterpret_cast<u32x4*>(q + 32) = l;
       }
     } else {
-      *reinterpret_cast<u32x4*>(a.hi + at) = raw;
+      *reinterpret_cast<u32x4*>(a.hi + at) = d0;  // dy as it lies (bf16)
     }
   }
   if (a.bsum == nullptr) return;
@@ -323,6 +318,64 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) s += cs[j][threadIdx.x];
   a.bsum[blockIdx.y * a.n + c] = s;
+}
+
+// The same where rows are not multiples of 16 bytes: a thread has one column, so that accesses of a row
+// are consecutive, and 16 rows at a time; 64 columns x 64 rows to a workgroup.
+template <bool kSplit>
+__global__ __launch_bounds__(256) void dz_ragged_kernel(const DzArgs a) {
+  __shared__ float cs[4][64];
+  int e = 0;
+  if constexpr (kSplit) {
+    e = scale_exp(a.parts);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.exp_out = e;
+  }
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kDzRows + 16 * (threadIdx.x >> 6);
+  float sum = 0.0f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float v[8], zv[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t row = r0 + 8 * half + j;
+      const bool in = row < a.m && col < a.n;
+      const int64_t o = in ? row * a.n + col : 0;
+      const float d = a.dy_f32 ? static_cast<const float*>(a.dy)[o] : bf16_val(static_cast<const uint16_t*>(a.dy)[o]);
+      v[j] = in ? d : 0.0f;
+      zv[j] = a.act != W4Q_ACT_NONE ? bf16_val(a.z[o]) : 0.0f;
+    }
+    switch (a.act) {
+      case W4Q_ACT_RELU: dact8<W4Q_ACT_RELU>(v, zv); break;
+      case W4Q_ACT_GELU: dact8<W4Q_ACT_GELU>(v, zv); break;
+      case W4Q_ACT_SILU: dact8<W4Q_ACT_SILU>(v, zv); break;
+      default: break;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t row = r0 + 8 * half + j;
+      if (row >= a.m || col >= a.np) continue;
+      if (col >= a.n) v[j] = 0.0f;  // (0 times another column's slope may be NaN)
+      sum += v[j];
+      if constexpr (kSplit) {
+        uint16_t h, l;
+        dz_split(v[j], e, h, l);
+        if (a.hi != nullptr) a.hi[row * a.np + col] = h;
+        if (a.both != nullptr) {
+          uint16_t* q = a.both + row * (2 * a.np) + (col >> 5) * 64 + (col & 31);
+          q[0] = h;
+          q[32] = l;
+        }
+      } else if (a.hi != nullptr) {
+        a.hi[row * a.np + col] = bf16_bits(v[j]);  // dy itself (bf16): exact
+      }
+    }
+  }
+  if (a.bsum == nullptr) return;
+  cs[threadIdx.x >> 6][threadIdx.x & 63] = sum;
+  __syncthreads();
+  if (threadIdx.x < 64 && col < a.n)
+    a.bsum[blockIdx.y * a.n + col] = (cs[0][threadIdx.x] + cs[1][threadIdx.x]) + (cs[2][threadIdx.x] + cs[3][threadIdx.x]);
 }
 
 // dbias: the tiles' column sums added in row order, in fp64 (one rounding at the end)
@@ -344,37 +397,19 @@ using Mid = NtCfg<128, 128, 64, 64, PA, 1, F16, AT, BT>;
 template <int PA, bool F16, bool AT, bool BT>
 using Small = NtCfg<64, 64, 32, 32, PA, 1, F16, AT, BT>;
 
-struct LinPlan {
-  int kind;  // 0 Big, 1 Mid, 2 Small
-  NtPlan p;
-};
-// Tile size by how many tiles there are: the largest one that still gives most compute units work.
-LinPlan lin_plan(int64_t M, int64_t N, int64_t K, int BK) {
-  LinPlan r;
-  r.p = nt_plan(1, M, N, K, false, 256, 256, BK, kNtCus);
-  r.kind = 0;
-  if (r.p.per_batch >= 96) return r;
-  r.p = nt_plan(1, M, N, K, false, 128, 128, BK, 2 * kNtCus);
-  r.kind = 1;
-  if (r.p.per_batch >= 128) return r;
-  r.p = nt_plan(1, M, N, K, false, 64, 64, BK, 4 * kNtCus);
-  r.kind = 2;
-  return r;
-}
-
-// a plan whose partial tiles fit ws_bytes: the plan itself, or one tile per workgroup
-void fit_plan(LinPlan& r, size_t ws_bytes) {
-  if (r.p.ws <= ws_bytes) return;
-  r.p.chunk = r.p.S;
-  r.p.nblk = r.p.total / r.p.S;
-  r.p.ws = 0;
+// parts: of the first operand; tiny: whether the small-product kernel takes the form (both along k)
+NtPlan lin_plan(int64_t M, int64_t N, int64_t K, int parts, bool tiny, bool split = true) {
+  return nt_plan(1, M, N, K, false, parts == 1 ? 64 : 32, parts == 1 ? 2.0 : 1.8, split, tiny);
 }
 
 template <int PA, bool F16, bool AT, bool BT, class Epi>
-int lin_product(const NtArgs& g, const LinPlan& r, const Epi& e, void* ws, hipStream_t s) {
-  if (r.kind == 0) return nt_launch<Big<PA, F16, AT, BT>, Epi>(g, r.p, 0, e, ws, s);
-  if (r.kind == 1) return nt_launch<Mid<PA, F16, AT, BT>, Epi>(g, r.p, 0, e, ws, s);
-  return nt_launch<Small<PA, F16, AT, BT>, Epi>(g, r.p, 0, e, ws, s);
+int lin_product(const NtArgs& g, const NtPlan& p, const Epi& e, void* ws, hipStream_t s) {
+  if (p.kind == 0) return nt_launch<Big<PA, F16, AT, BT>, Epi>(g, p, 0, e, ws, s);
+  if (p.kind == 1) return nt_launch<Mid<PA, F16, AT, BT>, Epi>(g, p, 0, e, ws, s);
+  if constexpr (!AT && !BT) {
+    if (p.kind == 3) return nt_launch_tiny<NtTinyCfg<PA, 1, F16, AT, BT>, Epi>(g, p, 0, e, s);
+  }
+  return nt_launch<Small<PA, F16, AT, BT>, Epi>(g, p, 0, e, ws, s);
 }
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -385,7 +420,7 @@ struct BwdLayout {
   bool split;        // dz in two fp16 parts
   bool direct;       // the products read dy as it lies
   int64_t np, mt;
-  LinPlan px, pw;
+  NtPlan px, pw;
   size_t parts, exps, hi, both, x16, w16, bsum, part, total;
 };
 BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
@@ -394,8 +429,8 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   l.np = up32(n);
   l.mt = (m + kDzRows - 1) / kDzRows;
   l.direct = !l.split && l.np == n;
-  l.px = lin_plan(m, k, l.np, 64);
-  l.pw = lin_plan(n, k, m, l.split ? 32 : 64);
+  l.px = lin_plan(m, k, l.np, 1, false);
+  l.pw = lin_plan(n, k, m, l.split ? 2 : 1, false);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -409,16 +444,37 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   l.x16 = take(l.split ? size_t(2) * m * k : 0);
   l.w16 = take(l.split ? size_t(2) * n * k : 0);
   l.bsum = take(sizeof(float) * l.mt * n);
-  const size_t most = l.px.p.ws > l.pw.p.ws ? l.px.p.ws : l.pw.p.ws;
+  const size_t most = l.px.ws > l.pw.ws ? l.px.ws : l.pw.ws;
   l.part = take(most);
   l.total = o;
   return l;
 }
 
+// The deployed weights as w4a16_gemm_dq reads them, bf16_RNE(s * q), written out for the product of many
+// rows: a group of 32 codes (16 bytes) per thread, s * (q + 8) - 8 s in one exact fused multiply-add.
+// HBM bound: 2.6 B per weight.
+__global__ __launch_bounds__(256) void dequant_kernel(const u32x4* __restrict__ packed, const uint16_t* __restrict__ s16,
+                                                      int64_t groups, u32x4* __restrict__ w) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= groups) return;
+  const u32x4 c = packed[i];
+  const float s = f16_bits_to_f32(s16[i]), ms = -8.0f * s;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint32_t word = c[d] ^ 0x88888888u;  // codes in offset binary
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(s, static_cast<float>((word >> (4 * e)) & 15u), ms);
+    w[4 * i + d] = pack_bf16(v);
+  }
+}
+
 // row lengths whose 256-row tiles stay within 32-bit buffer offsets, and iteration counts of the products
+constexpr int64_t kMaxIterations = 0x3FFFFFFF;
+int64_t most_iterations(int64_t M, int64_t N, int64_t K) { return nt_plan_tile(2, 1, M, N, K, false, 32).total; }
 bool fits(int64_t M, int64_t N, int64_t K) {
   if (M > 0x3FFFFFFF || N > 0x3FFFFFFF || K > (1 << 21)) return false;
-  return lin_plan(M, N, K, 32).p.total <= 0x3FFFFFFF;
+  return most_iterations(M, N, K) <= kMaxIterations;
 }
 
 }  // namespace
@@ -430,10 +486,10 @@ bool w4q_linear_fits(int64_t m, int64_t d_out, int64_t d_in, bool backward) {
   if (!backward) return fits(m, d_out, d_in);
   // one workgroup per 64 rows in the pass over dz; 32 rows of an operand within 32-bit buffer offsets
   if ((m + kDzRows - 1) / kDzRows > 65535 || d_in > (1 << 21)) return false;
-  return fits(m, d_in, up32(d_out)) && lin_plan(d_out, d_in, m, 32).p.total <= 0x3FFFFFFF;
+  return fits(m, d_in, up32(d_out)) && most_iterations(d_out, d_in, m) <= kMaxIterations;
 }
 
-size_t w4q_linear_fwd_workspace(int64_t m, int64_t d_out, int64_t d_in) { return lin_plan(m, d_out, d_in, 64).p.ws; }
+size_t w4q_linear_fwd_workspace(int64_t m, int64_t d_out, int64_t d_in) { return lin_plan(m, d_out, d_in, 1, true).ws; }
 size_t w4q_linear_bwd_workspace(int64_t m, int64_t d_out, int64_t d_in, int dy_f32, int act) {
   return bwd_layout(m, d_out, d_in, dy_f32, act).total;
 }
@@ -441,8 +497,8 @@ size_t w4q_linear_bwd_workspace(int64_t m, int64_t d_out, int64_t d_in, int dy_f
 int w4q_launch_linear_fwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,
                           const float* bias, int act, const void* res, uint16_t* z, void* y, int y_dtype, void* ws,
                           size_t ws_bytes, hipStream_t s) {
-  LinPlan p = lin_plan(m, d_out, d_in, 64);
-  fit_plan(p, ws != nullptr ? ws_bytes : 0);
+  NtPlan p = lin_plan(m, d_out, d_in, 1, true);
+  if (p.ws > (ws != nullptr ? ws_bytes : 0)) p = lin_plan(m, d_out, d_in, 1, true, false);
   NtArgs g = {};
   g.a = x;
   g.b = w_hat;
@@ -452,6 +508,28 @@ int w4q_launch_linear_fwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   const bool vec = d_out % 8 == 0 && at16(y) && at16(z) && at16(res);
   const EpiLinear e = {{bias, res, act}, z, y, y_dtype, vec ? 1 : 0};
   return lin_product<1, false, false, false>(g, p, e, ws, s);
+}
+
+// Rows from which w4a16_linear writes the dequantised weights out and runs the layer product on them,
+// rather than dequantising in the product's registers (gemm.hip).  DQMEASURED
+constexpr int64_t kDqRows = 17;
+size_t w4q_linear_dq_workspace(int64_t m, int64_t d_out, int64_t d_in) {
+  if (m < kDqRows || d_in % 256 != 0 || !fits(m, d_out, d_in)) return 0;
+  return up256(size_t(2) * d_out * d_in) + lin_plan(m, d_out, d_in, 1, true).ws;
+}
+
+int w4q_launch_linear_dq(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16, int64_t d_out,
+                         int64_t d_in, const W4Epilogue& ep, void* y, int y_dtype, void* ws, size_t ws_bytes,
+                         hipStream_t s) {
+  const int64_t groups = d_out * (d_in / 32);
+  uint16_t* w = static_cast<uint16_t*>(ws);
+  const size_t used = up256(size_t(2) * d_out * d_in);
+  hipLaunchKernelGGL(dequant_kernel, dim3(static_cast<unsigned>((groups + 255) / 256)), dim3(256), 0, s,
+                     reinterpret_cast<const u32x4*>(packed), s16, groups, reinterpret_cast<u32x4*>(w));
+  const int rc = w4q_launch_status();
+  if (rc != W4Q_OK) return rc;
+  return w4q_launch_linear_fwd(x, m, w, d_out, d_in, ep.bias, ep.act, ep.res, nullptr, y, y_dtype,
+                               static_cast<uint8_t*>(ws) + used, ws_bytes - used, s);
 }
 
 int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,
@@ -477,14 +555,15 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   }
   const bool need = products && !l.direct;
   if (need || db != nullptr) {
-    const bool vec = d_out % 8 == 0 && at16(z);
-    const DzArgs a = {dy, dy_f32, z, act, vec ? 1 : 0, m, d_out, l.np, need && (dx != nullptr || !l.split) ? u16(l.hi) : nullptr,
+    const DzArgs a = {dy, dy_f32, z, act, m, d_out, l.np, need && (dx != nullptr || !l.split) ? u16(l.hi) : nullptr,
                       l.split && dw != nullptr ? u16(l.both) : nullptr, bsum, parts, exps};
-    const dim3 grid(static_cast<unsigned>((l.np + 255) / 256), static_cast<unsigned>(l.mt));
+    const bool whole = d_out % 8 == 0 && at16(z);
+    const dim3 grid(static_cast<unsigned>(whole ? (l.np + 255) / 256 : (l.np + 63) / 64), static_cast<unsigned>(l.mt));
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
     if (l.split && need)
-      hipLaunchKernelGGL(dz_kernel<true>, grid, dim3(256), 0, s, a);
+      whole ? run(dz_kernel<true>) : run(dz_ragged_kernel<true>);
     else
-      hipLaunchKernelGGL(dz_kernel<false>, grid, dim3(256), 0, s, a);
+      whole ? run(dz_kernel<false>) : run(dz_ragged_kernel<false>);
     if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
   }
   if (db != nullptr) {

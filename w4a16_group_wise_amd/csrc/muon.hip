@@ -90,12 +90,16 @@ __device__ __forceinline__ Pair8 load_pair(const Split& m, int batch, int row, i
 // others get the transposed values
 template <bool kSym>
 struct EpiSplit {
-  static constexpr bool kMirror = kSym, kAhead = true;
+  static constexpr bool kMirror = kSym;
+  static constexpr int kLoads = 2;
   using Pre = Pair8;
   Split c;  // C term; c.p null: none
   float alpha, beta;
   Split o;
 
+  __device__ __forceinline__ bool whole() const { return true; }
+  __device__ __forceinline__ float load1(const NtArgs&, int, int, int) const { return 0.0f; }
+  __device__ __forceinline__ void store1(const NtArgs&, int, int, int, const float (&)[8], const float (&)[8]) const {}
   __device__ __forceinline__ Pre load(const NtArgs& g, int batch, int row, int col) const {
     Pre p = {};
     if (c.p != nullptr && row < g.M && col < c.ld) p = load_pair(c, batch, row, col);
@@ -115,7 +119,8 @@ struct EpiSplit {
 
 // the last update: o = (alpha * X + beta * acc) 2^-13, stored as the result or applied to the weights
 struct EpiLast {
-  static constexpr bool kMirror = false, kAhead = false;
+  static constexpr bool kMirror = false;
+  static constexpr int kLoads = 1;
   struct Pre {
     Pair8 x;
     u32x4 w0, w1;
@@ -128,11 +133,13 @@ struct EpiLast {
   float lr, scale, wd;
   int vec;        // 8 columns of a row may be moved in 16-byte pieces
 
+  __device__ __forceinline__ bool whole() const { return vec != 0; }
   __device__ __forceinline__ Pre load(const NtArgs& g, int batch, int row, int col) const {
     Pre p = {};
-    if (row < g.M && col < x.ld) p.x = load_pair(x, batch, row, col);
-    if (w != nullptr && vec && row < g.M && col < g.N)
-      load8(w, (static_cast<int64_t>(batch) * g.M + row) * g.N + col, 0, p.w0, p.w1);
+    if (vec && row < g.M && col < g.N) {
+      p.x = load_pair(x, batch, row, col);
+      if (w != nullptr) load8(w, (static_cast<int64_t>(batch) * g.M + row) * g.N + col, 0, p.w0, p.w1);
+    }
     return p;
   }
   __device__ __forceinline__ void store(const NtArgs& g, int batch, int row, int col, float (&v)[8], const Pre& p) const {
@@ -144,19 +151,32 @@ struct EpiLast {
     for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(alpha, t[e], beta * v[e]) * kSplitInv;
     if (w != nullptr) {
       unpack8(p.w0, p.w1, 0, wv);
-      if (!vec)
-        for (int e = 0; e < 8; ++e)
-          if (col + e < g.N) wv[e] = w[o + e];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = wv[e] - lr * (scale * v[e] + wd * wv[e]);
-    }
-    void* to = w != nullptr ? static_cast<void*>(w) : out;
-    const int dt = w != nullptr ? 0 : out_dtype;
-    if (vec) {
-      store8(to, o, dt, v);
+      store8(w, o, 0, v);
     } else {
-      for (int e = 0; e < 8; ++e)
-        if (col + e < g.N) store1(to, o + e, dt, v[e]);
+      store8(out, o, out_dtype, v);
+    }
+  }
+  __device__ __forceinline__ float load1(const NtArgs& g, int batch, int row, int col) const {
+    if (row >= g.M || col >= g.N) return 0.0f;
+    const uint16_t* q = x.p + x.at(batch, row, col);
+    return f16_bits_to_f32(q[0]) + f16_bits_to_f32(q[32]);
+  }
+  __device__ __forceinline__ void store1(const NtArgs& g, int batch, int row, int col, const float (&v)[8],
+                                         const float (&t)[8]) const {
+    const int64_t o = (static_cast<int64_t>(batch) * g.M + row) * g.N + col;
+    float wv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wv[e] = w != nullptr && row + e < g.M ? w[o + static_cast<int64_t>(e) * g.N] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (row + e >= g.M) continue;
+      const float u = __builtin_fmaf(alpha, t[e], beta * v[e]) * kSplitInv;
+      if (w != nullptr)
+        w[o + static_cast<int64_t>(e) * g.N] = wv[e] - lr * (scale * u + wd * wv[e]);
+      else
+        w4q::store1(out, o + static_cast<int64_t>(e) * g.N, out_dtype, u);
     }
   }
 };
@@ -307,36 +327,22 @@ using Mid = NtCfg<128, 128, 64, 64, 2, 2, true, AT, BT>;
 template <bool AT, bool BT>
 using Small = NtCfg<64, 64, 32, 32, 2, 2, true, AT, BT, true>;
 
-struct NsPlan {
-  int kind;  // 0 Big, 1 Mid, 2 Small
-  NtPlan p;
-};
-
-// Tile size by how many tiles there are: the largest one that still gives most compute units work.
-NsPlan ns_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri) {
-  NsPlan r;
-  r.p = nt_plan(batch, M, N, K, tri, 256, 256, 32, kNtCus);
-  r.kind = 0;
-  if (batch * r.p.per_batch >= 96) return r;
-  r.p = nt_plan(batch, M, N, K, tri, 128, 128, 32, 2 * kNtCus);
-  r.kind = 1;
-  if (batch * r.p.per_batch >= 128) return r;
-  r.p = nt_plan(batch, M, N, K, tri, 64, 64, 32, 4 * kNtCus);
-  r.kind = 2;
-  return r;
+NtPlan ns_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri) {
+  return nt_plan(batch, M, N, K, tri, 32, 2.4, true, true);
 }
 
 template <bool AT, bool BT, class Epi>
-int ns_product(const NtArgs& g, const NsPlan& r, int tri, const Epi& e, void* ws, hipStream_t s) {
-  if (r.kind == 0) return nt_launch<Big<AT, BT>, Epi>(g, r.p, tri, e, ws, s);
-  if (r.kind == 1) return nt_launch<Mid<AT, BT>, Epi>(g, r.p, tri, e, ws, s);
-  return nt_launch<Small<AT, BT>, Epi>(g, r.p, tri, e, ws, s);
+int ns_product(const NtArgs& g, const NtPlan& p, int tri, const Epi& e, void* ws, hipStream_t s) {
+  if (p.kind == 0) return nt_launch<Big<AT, BT>, Epi>(g, p, tri, e, ws, s);
+  if (p.kind == 1) return nt_launch<Mid<AT, BT>, Epi>(g, p, tri, e, ws, s);
+  if (p.kind == 2) return nt_launch<Small<AT, BT>, Epi>(g, p, tri, e, ws, s);
+  return nt_launch_tiny<NtTinyCfg<2, 2, true, AT, BT, true>, Epi>(g, p, tri, e, s);
 }
 
 struct NsLayout {
   bool wide;            // rows <= cols
   int64_t n, np, ld;    // the smaller side, padded; X's row length (cols, padded)
-  NsPlan gram, poly, upd;
+  NtPlan gram, poly, upd;
   int parts;
   size_t sums, x0, x1, aa, bb, part, total;  // byte offsets, end
 };
@@ -367,7 +373,7 @@ NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
   l.aa = take(n_bytes);
   l.bb = take(n_bytes);
   size_t most = 0;
-  for (const NsPlan* p : {&l.gram, &l.poly, &l.upd}) most = p->p.ws > most ? p->p.ws : most;
+  for (const NtPlan* p : {&l.gram, &l.poly, &l.upd}) most = p->ws > most ? p->ws : most;
   l.part = take(most);
   l.total = o;
   return l;
@@ -381,8 +387,8 @@ using namespace w4q;
 bool w4q_ns_fits(int64_t batch, int64_t rows, int64_t cols) {
   if (batch > 65535 || rows > 131072 || cols > 131072) return false;
   const NsLayout l = ns_layout(batch, rows, cols);
-  for (const NsPlan* p : {&l.gram, &l.poly, &l.upd})
-    if (p->p.total > 0x3FFFFFFF) return false;
+  for (const NtPlan* p : {&l.gram, &l.poly, &l.upd})
+    if (p->total > 0x3FFFFFFF) return false;
   return true;
 }
 

@@ -94,6 +94,16 @@ __device__ __forceinline__ void nt_tile(const NtArgs& g, int t, int& batch, int&
   }
 }
 
+template <int N>
+__device__ __forceinline__ void nt_dma(uint32_t lds, v4i32 rs, const int (&vo)[N]) {
+  if constexpr (N == 4)
+    dma_x4(lds, rs, vo);
+  else if constexpr (N == 2)
+    dma_x2(lds, rs, vo[0], vo[1]);
+  else
+    dma_x1(lds, rs, vo[0]);
+}
+
 // An operand's tile in LDS: W rows (along) or columns (across), P parts, BK k a stage
 template <int W, int P, bool kAcross, int BK, int kWaves>
 struct NtOperand {
@@ -109,6 +119,34 @@ struct NtOperand {
     const int r = u * kRows + lane / kChunks;
     const int c = (lane % kChunks) ^ (kAcross ? nt_tswz<kRow>(r) : nt_swz(r));
     return r * ld * 2 + 16 * c;
+  }
+  // This wavefront's loads of stage s to `dst`: loads u0 .. u0 + kLoads - 1 of the tile whose first row
+  // (along) or column (across) is r0, vo their load_off.  rows: the operand's rows (along) or k rows
+  // (across).  !live: empty loads, which write zeros.
+  static __device__ __forceinline__ void issue(const uint16_t* base, int s, bool live, int r0, int rows, int ld, int K,
+                                               uint32_t dst, int u0, int lane, const int (&vo)[kLoads]) {
+    int64_t off;
+    int bytes;
+    if constexpr (kAcross) {
+      const int left = rows - BK * s;
+      off = static_cast<int64_t>(BK * s) * ld + r0 * P;
+      bytes = ((left < BK ? left : BK) * ld - r0 * P) * 2;
+    } else {
+      const int left = rows - r0;
+      off = static_cast<int64_t>(r0) * ld + 64 * s;
+      bytes = ((left < W ? left : W) * ld - 64 * s) * 2;
+    }
+    const v4i32 rs = buffer_rsrc(base + (live ? off : 0), live ? bytes : 0);
+    if (BK == 64 && !kAcross && K - 64 * s == 32) {
+      // half a stage: the second 32 k of each row (chunks 4..7) lie beyond K and read as zeros
+      int half[kLoads];
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q)
+        half[q] = ((lane ^ nt_swz(8 * (u0 + q) + (lane >> 3))) & 4) != 0 ? 0x7FFFFFF0 : vo[q];
+      nt_dma(dst, rs, half);
+    } else {
+      nt_dma(dst, rs, vo);
+    }
   }
   // byte offset in the tile of this lane's fragment of rows r0 .. r0 + 31, first step, first part
   static __device__ __forceinline__ int read_off(int r0, int lane) {
@@ -174,10 +212,15 @@ __device__ __forceinline__ int64_t nt_part_off(int w, int blk, int q, int lane) 
 // ---------------------------------------------------------------------------- epilogue strips
 // A strip is 32 rows x WN columns of a wavefront's tile.  Lane l takes 8 columns from 8 (l % (WN / 8)) of
 // rows l / (WN / 8) + kRows i.  The functor gives, for 8 columns of one row:
-//   Pre load(g, batch, row, col)                     what the epilogue reads there (kAhead: one strip
-//                                                    ahead of its use, in twice the registers)
+//   Pre load(g, batch, row, col)                     what the epilogue reads there.  kLoads: 2 the next
+//                                                    strip's before a strip is stored, 1 after, 0 a
+//                                                    pass ahead, in a loop (for long epilogues, whose
+//                                                    unrolled code would spill accumulators)
 //   void store(g, batch, row, col, v[8], pre)        writes the outputs; leaves in v what a mirrored
 //                                                    store shall write
+//   bool whole()                                     false: rows are not multiples of 16 bytes, and
+//   float load1(g, batch, row, col)                  the epilogue runs on 8 rows of one column
+//   void store1(g, batch, row, col, v[8], x[8])      (x: load1 of each row)
 //   kMirror, void store_t(g, batch, col, row, v[8])  symmetric results: 8 rows of one column
 template <class C>
 struct NtStrip {
@@ -195,29 +238,63 @@ __device__ __forceinline__ void nt_strip_load(const NtArgs& g, const Epi& epi, i
     pre[i] = epi.load(g, batch, row0 + lane / S::kLanes + S::kRows * i, col0 + 8 * (lane % S::kLanes));
 }
 
-template <class C, class Epi>
-__device__ __forceinline__ void nt_strip_store(const NtArgs& g, const Epi& epi, int batch, int row0, int col0, bool diag,
-                                               const f32x16 (&acc)[C::NB], int lane, float* buf,
-                                               const typename Epi::Pre (&pre)[NtStrip<C>::kPasses]) {
-  using S = NtStrip<C>;
-  // accumulator layout: lane l, register r -> row 8(r/4) + 4(l/32) + r%4, column l%32
+// one strip of accumulators to LDS: lane l, register r -> row 8(r/4) + 4(l/32) + r%4, column l%32
+template <class C>
+__device__ __forceinline__ void nt_strip_write(const f32x16 (&acc)[C::NB], int lane, float* buf) {
 #pragma unroll
   for (int j = 0; j < C::NB; ++j)
 #pragma unroll
     for (int r = 0; r < 16; ++r)
       buf[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * C::kPitch + 32 * j + (lane & 31)] = acc[j][r];
+}
+
+template <class C, class Epi>
+__device__ __forceinline__ void nt_strip_store(const NtArgs& g, const Epi& epi, int batch, int row0, int col0, bool diag,
+                                               int lane, float* buf, const typename Epi::Pre (&pre)[NtStrip<C>::kPasses]) {
+  using S = NtStrip<C>;
   asm volatile("" ::: "memory");  // the wavefront's own LDS operations stay in order
+  if (!epi.whole()) {
+    // rows that are not multiples of 16 bytes: a lane has one column and 8 rows at a time, so that
+    // a wavefront's accesses of a row are still consecutive
+    constexpr int kHalves = 64 / C::WN;  // row groups side by side
+    const int col = col0 + lane % C::WN;
+#pragma unroll 1
+    for (int i = 0; i < 4 / kHalves; ++i) {
+      const int rl = 8 * (i * kHalves + lane / C::WN);
+      float v[8], x[8];
 #pragma unroll
-  for (int i = 0; i < S::kPasses; ++i) {
+      for (int e = 0; e < 8; ++e) {
+        v[e] = buf[(rl + e) * C::kPitch + lane % C::WN];
+        x[e] = epi.load1(g, batch, row0 + rl + e, col);
+      }
+      if (col < g.N) epi.store1(g, batch, row0 + rl, col, v, x);
+    }
+    asm volatile("" ::: "memory");
+    return;
+  }
+  auto pass = [&](int i, const typename Epi::Pre& x) {
     const int rl = lane / S::kLanes + S::kRows * i, cl = 8 * (lane % S::kLanes);
     float* p = buf + rl * C::kPitch + cl;
     const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
     float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    epi.store(g, batch, row0 + rl, col0 + cl, v, pre[i]);
+    epi.store(g, batch, row0 + rl, col0 + cl, v, x);
     if constexpr (Epi::kMirror) {
       *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
       *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
     }
+  };
+  if constexpr (Epi::kLoads == 0) {
+    auto at = [&](int i) { return epi.load(g, batch, row0 + lane / S::kLanes + S::kRows * i, col0 + 8 * (lane % S::kLanes)); };
+    typename Epi::Pre x = at(0);
+#pragma unroll 1
+    for (int i = 0; i < S::kPasses; ++i) {
+      const typename Epi::Pre next = i + 1 < S::kPasses ? at(i + 1) : x;
+      pass(i, x);
+      x = next;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < S::kPasses; ++i) pass(i, pre[i]);
   }
   if constexpr (Epi::kMirror) {
     if (!diag) {
@@ -233,16 +310,6 @@ __device__ __forceinline__ void nt_strip_store(const NtArgs& g, const Epi& epi, 
     }
   }
   asm volatile("" ::: "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void nt_dma(uint32_t lds, v4i32 rs, const int (&vo)[N]) {
-  if constexpr (N == 4)
-    dma_x4(lds, rs, vo);
-  else if constexpr (N == 2)
-    dma_x2(lds, rs, vo[0], vo[1]);
-  else
-    dma_x1(lds, rs, vo[0]);
 }
 
 template <class C, class Epi>
@@ -282,41 +349,13 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     const uint16_t* abase = g.a + batch * g.sa;
     const uint16_t* bbase = g.b + batch * g.sb;
 
-    // an operand's loads of stage s (past the range: empty loads, which write zeros)
-    auto issue_op = [&](const uint16_t* base, int s, int r0, int rows, int ld, int krows, uint32_t dst, auto op, int width,
-                        int parts, bool across, const auto& vo) {
-      using Op = decltype(op);
-      const bool live = s < s1;
-      int64_t off;
-      int bytes;
-      if (across) {
-        const int left = krows - C::BK * s;
-        off = static_cast<int64_t>(C::BK * s) * ld + r0 * parts;
-        bytes = ((left < C::BK ? left : C::BK) * ld - r0 * parts) * 2;
-      } else {
-        const int left = rows - r0;
-        off = static_cast<int64_t>(r0) * ld + 64 * s;
-        bytes = ((left < width ? left : width) * ld - 64 * s) * 2;
-      }
-      const v4i32 rs = buffer_rsrc(base + (live ? off : 0), live ? bytes : 0);
-      const uint32_t to = dst + wid * (Op::kLoads * 1024);
-      if (C::BK == 64 && !across && g.K - 64 * s == 32) {
-        // half a stage: the second 32 k of each row (chunks 4..7) lie beyond K and read as zeros
-        int half[Op::kLoads];
-#pragma unroll
-        for (int q = 0; q < Op::kLoads; ++q) {
-          const int r = 8 * (wid * Op::kLoads + q) + (lane >> 3);
-          half[q] = ((lane ^ nt_swz(r)) & 4) != 0 ? 0x7FFFFFF0 : vo[q];
-        }
-        nt_dma(to, rs, half);
-      } else {
-        nt_dma(to, rs, vo);
-      }
-    };
+    // loads of stage s into buffer `buf` (past the range: empty)
     auto issue = [&](int s, int buf) {
       const uint32_t dst = lds0 + buf * C::kStage;
-      issue_op(abase, s, m0, g.M, g.lda, g.ka, dst, OpA{}, C::BM, C::PA, C::AT, avo);
-      issue_op(bbase, s, n0, g.N, g.ldb, g.kb, dst + OpA::kBytes, OpB{}, C::BN, C::PB, C::BT, bvo);
+      OpA::issue(abase, s, s < s1, m0, C::AT ? g.ka : g.M, g.lda, g.K, dst + wid * (OpA::kLoads * 1024), wid * OpA::kLoads,
+                 lane, avo);
+      OpB::issue(bbase, s, s < s1, n0, C::BT ? g.kb : g.N, g.ldb, g.K, dst + OpA::kBytes + wid * (OpB::kLoads * 1024),
+                 wid * OpB::kLoads, lane, bvo);
     };
 
     f32x16 acc[C::MB][C::NB];
@@ -402,14 +441,15 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     if (s0 == 0 && s1 == g.S) {
       float* strip = reinterpret_cast<float*>(lds + wid * (C::kLds / C::kWaves));
       const int row0 = m0 + wm * C::WM, col0 = n0 + wn * C::WN;
-      constexpr int kSets = Epi::kAhead ? 2 : 1;
+      constexpr int kSets = Epi::kLoads == 2 ? 2 : 1;
       typename Epi::Pre pre[kSets][NtStrip<C>::kPasses];
-      nt_strip_load<C>(g, epi, batch, row0, col0, lane, pre[0]);
+      if (Epi::kLoads != 0) nt_strip_load<C>(g, epi, batch, row0, col0, lane, pre[0]);
 #pragma unroll
       for (int i = 0; i < C::MB; ++i) {
         if (kSets == 2 && i + 1 < C::MB) nt_strip_load<C>(g, epi, batch, row0 + 32 * (i + 1), col0, lane, pre[(i + 1) % kSets]);
-        nt_strip_store<C>(g, epi, batch, row0 + 32 * i, col0, ti == tj, acc[i], lane, strip, pre[i % kSets]);
-        if (kSets == 1 && i + 1 < C::MB) nt_strip_load<C>(g, epi, batch, row0 + 32 * (i + 1), col0, lane, pre[0]);
+        nt_strip_write<C>(acc[i], lane, strip);
+        nt_strip_store<C>(g, epi, batch, row0 + 32 * i, col0, ti == tj, lane, strip, pre[i % kSets]);
+        if (Epi::kLoads == 1 && i + 1 < C::MB) nt_strip_load<C>(g, epi, batch, row0 + 32 * (i + 1), col0, lane, pre[0]);
       }
       if (it + (s1 - s0) < it_end) sync(std::integral_constant<int, 0>{});  // the next tile's loads reuse the LDS
     } else {
@@ -448,7 +488,7 @@ __global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi 
   const int row0 = ti * C::BM + (wid / C::kWavesN) * C::WM + 32 * i;
   const int col0 = tj * C::BN + (wid % C::kWavesN) * C::WN;
   typename Epi::Pre pre[NtStrip<C>::kPasses];
-  nt_strip_load<C>(g, epi, batch, row0, col0, lane, pre);
+  if (Epi::kLoads != 0) nt_strip_load<C>(g, epi, batch, row0, col0, lane, pre);
   f32x16 v[C::NB];
 #pragma unroll
   for (int j = 0; j < C::NB; ++j)
@@ -466,7 +506,110 @@ __global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi 
         for (int e = 0; e < 4; ++e) v[j][4 * q + e] += x[e];
       }
   }
-  nt_strip_store<C>(g, epi, batch, row0, col0, ti == tj, v, lane, strip, pre);
+  nt_strip_write<C>(v, lane, strip);
+  nt_strip_store<C>(g, epi, batch, row0, col0, ti == tj, lane, strip, pre);
+}
+
+// ------------------------------------------------------------------------------- small products
+// For products too small to fill the device with tiles of 64: 32x32 tiles, the stages of a tile dealt
+// to the 8 wavefronts of a workgroup, each with LDS buffers of its own (no barrier until the end, all
+// loads of a short sum in flight at once), the wavefronts' sums added in LDS in a fixed order.  256 x 512
+// Newton-Schulz products: 8 us each on 64x64 tiles, LDSUS us here.
+template <int PA_, int PB_, bool F16_, bool AT_, bool BT_, bool LOLO_ = false>
+struct NtTinyCfg {
+  static constexpr int BM = 32, BN = 32, WM = 32, WN = 32, PA = PA_, PB = PB_;
+  static constexpr bool F16 = F16_, AT = AT_, BT = BT_, LOLO = LOLO_;
+  static constexpr int BK = PA == 1 && PB == 1 ? 64 : 32, KS = BK / 16;
+  static constexpr int kWaves = 8, kThreads = 64 * kWaves, MB = 1, NB = 1;
+  using OpA = NtOperand<32, PA, AT, BK, 1>;
+  using OpB = NtOperand<32, PB, BT, BK, 1>;
+  static constexpr int kOps = OpA::kLoads + OpB::kLoads;
+  static constexpr int kStage = OpA::kBytes + OpB::kBytes;
+  static constexpr int kLds = 2 * kStage * kWaves;
+  static constexpr int kPitch = WN + 4;
+  static_assert(2 * kStage >= 32 * kPitch * 4 && kLds <= 160 * 1024, "LDS");
+};
+
+template <class C, class Epi>
+__global__ __launch_bounds__(C::kThreads) void nt_tiny_kernel(const NtArgs g, const Epi epi) {
+  using OpA = typename C::OpA;
+  using OpB = typename C::OpB;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
+  const int t = static_cast<int>(blockIdx.x & 7) * g.per_xcd + static_cast<int>(blockIdx.x >> 3);
+  if (t >= g.nblk) return;
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  uint8_t* mine = lds + wid * (2 * C::kStage);
+  const uint32_t lds0 = lds_addr(lds) + wid * (2 * C::kStage);
+  int batch, ti, tj;
+  nt_tile(g, t, batch, ti, tj);
+  const int m0 = ti * 32, n0 = tj * 32;
+  const uint16_t* abase = g.a + batch * g.sa;
+  const uint16_t* bbase = g.b + batch * g.sb;
+  int avo[OpA::kLoads], bvo[OpB::kLoads];
+#pragma unroll
+  for (int q = 0; q < OpA::kLoads; ++q) avo[q] = OpA::load_off(q, lane, g.lda);
+#pragma unroll
+  for (int q = 0; q < OpB::kLoads; ++q) bvo[q] = OpB::load_off(q, lane, g.ldb);
+  const int aro = OpA::read_off(0, lane), bro = OpB::read_off(0, lane);
+  auto issue = [&](int s, int buf) {
+    const uint32_t dst = lds0 + buf * C::kStage;
+    OpA::issue(abase, s, s < g.S, m0, C::AT ? g.ka : g.M, g.lda, g.K, dst, 0, lane, avo);
+    OpB::issue(bbase, s, s < g.S, n0, C::BT ? g.kb : g.N, g.ldb, g.K, dst + OpA::kBytes, 0, lane, bvo);
+  };
+  f32x16 acc[1];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[0][r] = 0.0f;
+  issue(wid, 0);
+  issue(wid + C::kWaves, 1);
+  int buf = 0;
+  for (int s = wid; s < g.S; s += C::kWaves) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(C::kOps));  // this stage's loads (the wavefront's own buffer)
+    asm volatile("" ::: "memory");
+    const uint8_t* pa = mine + buf * C::kStage;
+    const uint8_t* pb = pa + OpA::kBytes;
+    u32x4 a[C::KS][C::PA], b[C::KS][C::PB];
+#pragma unroll
+    for (int kk = 0; kk < C::KS; ++kk) {
+#pragma unroll
+      for (int p = 0; p < C::PA; ++p) a[kk][p] = OpA::read(pa, aro, kk, p);
+#pragma unroll
+      for (int p = 0; p < C::PB; ++p) b[kk][p] = OpB::read(pb, bro, kk, p);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(waitcnt_lgkm0());  // the buffer has been read
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    issue(s + 2 * C::kWaves, buf);
+#pragma unroll
+    for (int kk = 0; kk < C::KS; ++kk) {
+      if constexpr (C::LOLO) acc[0] = nt_mfma<C::F16>(a[kk][C::PA - 1], b[kk][C::PB - 1], acc[0]);
+      if constexpr (C::PB == 2) acc[0] = nt_mfma<C::F16>(a[kk][0], b[kk][1], acc[0]);
+      if constexpr (C::PA == 2) acc[0] = nt_mfma<C::F16>(a[kk][1], b[kk][0], acc[0]);
+      acc[0] = nt_mfma<C::F16>(a[kk][0], b[kk][0], acc[0]);
+    }
+    buf ^= 1;
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing is on its way to the buffers
+  asm volatile("" ::: "memory");
+  nt_strip_write<C>(acc, lane, reinterpret_cast<float*>(mine));
+  __syncthreads();
+  float* strip = reinterpret_cast<float*>(lds);
+  constexpr int kStride = 2 * C::kStage / 4;  // floats between the wavefronts' strips
+  for (int e = threadIdx.x; e < 32 * 32; e += C::kThreads) {
+    const int at = (e >> 5) * C::kPitch + (e & 31);
+    float v = strip[at];
+#pragma unroll
+    for (int w = 1; w < C::kWaves; ++w) v += strip[w * kStride + at];
+    strip[at] = v;
+  }
+  typename Epi::Pre pre[NtStrip<C>::kPasses];
+  if (wid == 0 && Epi::kLoads != 0) nt_strip_load<C>(g, epi, batch, m0, n0, lane, pre);
+  __syncthreads();
+  if (wid == 0) nt_strip_store<C>(g, epi, batch, m0, n0, ti == tj, lane, strip, pre);
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -474,37 +617,83 @@ constexpr int kNtCus = 256;
 constexpr int kNtMinK = 512;  // k a range covers at least
 
 struct NtPlan {
+  int kind;  // tile: 0 256x256, 1 128x128, 2 64x64, 3 32x32 (small products)
   int64_t tm, tn, per_batch, S, total, chunk, nblk;
   size_t ws;  // scratch bytes (0: no tile is split)
 };
 
-// The split of `batch` products of M x N x K on BM x BN tiles where `slots` workgroups run at once:
-// one tile per workgroup when the tiles fill (nearly) whole rounds of the device, else equal
-// ranges of stages, one per slot.
-inline NtPlan nt_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, int BM, int BN, int BK, int slots) {
+// What a tile costs, in units of a 256x256 tile's stage on a fully busy device (2.4 us for 2 x 2
+// parts, 2.0 for 64 k of 1 x 1, 1.8 for 2 x 1): `busy` per tile and stage when a compute unit
+// always has a tile to work on, `alone` with one tile on it; measured on 4096, 2048 and 1024 cubed.
+struct NtTile {
+  int edge, per_cu;
+  double busy, alone;
+};
+constexpr NtTile kNtTiles[4] = {{256, 1, 1.0, 0.70}, {128, 2, 0.265, 0.35}, {64, 4, 0.098, 0.155}, {32, 1, 0.0, 0.0}};
+
+inline NtPlan nt_plan_tile(int kind, int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, int BK) {
   NtPlan p;
-  p.tm = (M + BM - 1) / BM;
-  p.tn = (N + BN - 1) / BN;
+  const int64_t edge = kNtTiles[kind].edge;
+  p.kind = kind;
+  p.tm = (M + edge - 1) / edge;
+  p.tn = (N + edge - 1) / edge;
   p.per_batch = tri ? p.tm * (p.tm + 1) / 2 : p.tm * p.tn;
   p.S = (K + BK - 1) / BK;
-  const int64_t tiles = batch * p.per_batch;
-  p.total = tiles * p.S;
+  p.total = batch * p.per_batch * p.S;
   p.chunk = p.S;
-  const int64_t rounds = (tiles + slots - 1) / slots;
-  if (tiles * 100 < rounds * slots * 85 && rounds <= 4) {
-    int64_t chunk = (p.total + slots - 1) / slots;
-    if (chunk < kNtMinK / BK) chunk = kNtMinK / BK;
-    if (chunk < p.S || (rounds > 1 && chunk < p.S * rounds)) p.chunk = chunk;
-  }
-  p.nblk = (p.total + p.chunk - 1) / p.chunk;
-  p.ws = p.chunk % p.S != 0 ? static_cast<size_t>(p.nblk) * 2 * BM * BN * sizeof(float) : 0;
+  p.nblk = batch * p.per_batch;
+  p.ws = 0;
   return p;
 }
 
+// The cheapest of: whole tiles of each size, and (split) equal ranges of stages of each size, whose
+// partial tiles then pass through memory once more (5 us and 3 TB/s measured).  Sizes with the same
+// estimate take the larger tile.  E.g. 2 x 2 parts at 2048 cubed: 112 us on 64 tiles of 256, 52 us on
+// 256 of 128, 59 us on 1024 of 64; 1024 cubed: 56, 22, 12 us; 512 x 512 x 8192: 398, 143, 106 us
+// whole and 42, 29, 30 us in ranges.
+inline NtPlan nt_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, int BK, double unit_us, bool split,
+                      bool tiny) {
+  NtPlan best = {};
+  double best_us = 0.0;
+  for (int kind = 0; kind < 3; ++kind) {
+    const NtTile& t = kNtTiles[kind];
+    NtPlan p = nt_plan_tile(kind, batch, M, N, K, tri, BK);
+    const int64_t tiles = p.nblk;
+    const double per_cu = static_cast<double>((tiles + kNtCus - 1) / kNtCus);
+    const double each = per_cu * t.busy > t.alone ? per_cu * t.busy : t.alone;
+    const double us = 4.0 + unit_us * static_cast<double>(p.S) * each;
+    if (kind == 0 || us < best_us) {
+      best = p;
+      best_us = us;
+    }
+    if (!split) continue;
+    const int64_t slots = kNtCus * t.per_cu;
+    int64_t chunk = (p.total + slots - 1) / slots;
+    if (chunk < kNtMinK / BK) chunk = kNtMinK / BK;
+    if (chunk % p.S == 0) continue;
+    p.chunk = chunk;
+    p.nblk = (p.total + chunk - 1) / chunk;
+    p.ws = static_cast<size_t>(p.nblk) * 2 * t.edge * t.edge * sizeof(float);
+    const double load = static_cast<double>(p.total) * t.busy / kNtCus;  // evenly spread
+    const double alone = static_cast<double>(chunk) * t.alone;
+    const double bytes = static_cast<double>(p.nblk + tiles) * t.edge * t.edge * 4.0;
+    const double sus = 9.0 + unit_us * (load > alone ? load : alone) + bytes / 3e6;
+    if (sus < best_us) {
+      best = p;
+      best_us = sus;
+    }
+  }
+  if (tiny) {
+    // a workgroup's round: a fixed 2 us and, for each of its 8 wavefronts, half a microsecond a stage
+    const NtPlan p = nt_plan_tile(3, batch, M, N, K, tri, BK);
+    const double us = 2.0 + static_cast<double>((p.nblk + kNtCus - 1) / kNtCus) * (2.0 + 0.5 * static_cast<double>((p.S + 7) / 8));
+    if (us < best_us) best = p;
+  }
+  return best;
+}
+
 // one product: fills in the plan, launches the product and, where tiles were split, the fixup
-template <class C, class Epi>
-int nt_launch(NtArgs g, const NtPlan& p, int tri, const Epi& epi, void* ws, hipStream_t s) {
-  if (p.total > 0x3FFFFFFF) return W4Q_EUNSUPPORTED;
+inline void nt_fill(NtArgs& g, const NtPlan& p, int tri, void* ws) {
   g.tm = static_cast<int>(p.tm);
   g.tn = static_cast<int>(p.tn);
   g.tri = tri;
@@ -515,6 +704,20 @@ int nt_launch(NtArgs g, const NtPlan& p, int tri, const Epi& epi, void* ws, hipS
   g.nblk = static_cast<int>(p.nblk);
   g.per_xcd = (g.nblk + 7) / 8;
   g.ws = static_cast<float*>(ws);
+}
+
+template <class C, class Epi>
+int nt_launch_tiny(NtArgs g, const NtPlan& p, int tri, const Epi& epi, hipStream_t s) {
+  if (p.total > 0x3FFFFFFF) return W4Q_EUNSUPPORTED;
+  nt_fill(g, p, tri, nullptr);
+  hipLaunchKernelGGL((nt_tiny_kernel<C, Epi>), dim3(static_cast<unsigned>(8 * g.per_xcd)), dim3(C::kThreads), 0, s, g, epi);
+  return w4q_launch_status();
+}
+
+template <class C, class Epi>
+int nt_launch(NtArgs g, const NtPlan& p, int tri, const Epi& epi, void* ws, hipStream_t s) {
+  if (p.total > 0x3FFFFFFF) return W4Q_EUNSUPPORTED;
+  nt_fill(g, p, tri, ws);
   hipLaunchKernelGGL((nt_kernel<C, Epi>), dim3(static_cast<unsigned>(8 * g.per_xcd)), dim3(C::kThreads), 0, s, g, epi);
   int rc = w4q_launch_status();
   if (rc == W4Q_OK && p.ws != 0) {

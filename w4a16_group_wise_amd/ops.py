@@ -8,6 +8,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import ctypes
+import functools
 import torch
 
 from ._lib import W4Q_GROUP, check, lib
@@ -56,8 +57,8 @@ def _workspace(query: str, sizes, device, workspace: Optional[torch.Tensor]):
 
 def workspace_size(op: str, *sizes) -> int:
     """Scratch bytes: op in ("quant_hessian", "w4a16_gemm", "w4a16_gemm_dq", "per_channel", "joint",
-    "gptq", "lsq_linear_fwd", "lsq_linear_bwd", "newton_schulz") with (n_tok, d), (m, d_out, d_in),
-    (d_out, d_in), (m, d_out, d_in, grad_y dtype, act) or (batch, rows, cols) as the C query takes them."""
+    "gptq", "lsq_linear_fwd", "lsq_linear_bwd", "w4a16_linear", "newton_schulz") with (n_tok, d), (m, d_out, d_in),
+    (d_out, d_in), (m, d_out, d_in, grad_y dtype, act), (m, d_out, d_in, w_mode) or (batch, rows, cols) as the C query takes them."""
     n = ctypes.c_size_t(0)
     check(op + "_workspace_size", getattr(lib(), op + "_workspace_size")(*sizes, ctypes.byref(n)))
     return n.value
@@ -374,6 +375,40 @@ def quant_gptq(w: torch.Tensor, h: torch.Tensor, scale: torch.Tensor, damp: floa
 NS_COEFFS = (3.4445, -4.7750, 2.0315)  # the published Muon coefficients
 
 
+class _OnDevice:
+    """The device of a call made current for it, where it is not already."""
+
+    def __init__(self, device: torch.device):
+        self._guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+@functools.lru_cache(maxsize=4096)
+def _need_bytes(query: str, sizes) -> int:
+    """A workspace query's answer (a function of the sizes alone)."""
+    n = ctypes.c_size_t(0)
+    check(query, getattr(lib(), query)(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+def _scratch(query: str, sizes, device, workspace: Optional[torch.Tensor]):
+    """As _workspace, with the query's answer remembered per size."""
+    if workspace is not None:
+        return _workspace(query, sizes, device, workspace)
+    n = _need_bytes(query, sizes)
+    if n == 0:
+        return None, 0, None
+    buf = torch.empty(n, dtype=torch.uint8, device=device)
+    return buf.data_ptr(), n, buf
+
+
 def _act(act: str) -> int:
     from ._lib import W4Q_ACTS
     if act not in W4Q_ACTS:
@@ -444,12 +479,12 @@ def lsq_linear_fwd(x: torch.Tensor, w: Optional[torch.Tensor], scale: Optional[t
             raise ValueError(f"w_hat must be [d_out][{d_in}], got {tuple(w_hat.shape)}")
         d_out = w_hat.shape[0]
     _epilogue(m, d_out, out_dtype, x.device, bias, residual)
-    with torch.cuda.device(x.device):
+    with _OnDevice(x.device):
         y = _out(out, "y", (m, d_out), out_dtype, x.device)
         z = torch.empty((m, d_out), dtype=torch.bfloat16, device=x.device) if with_z else None
         if out is not None:
             _no_overlap((((y, "out"), (t, n)) for t, n in ((x, "x"), (w, "w"), (w_hat, "w_hat"))))
-        wp, wb, _keep = _workspace("lsq_linear_fwd_workspace_size", (m, d_out, d_in), x.device, workspace)
+        wp, wb, _keep = _scratch("lsq_linear_fwd_workspace_size", (m, d_out, d_in), x.device, workspace)
         check("lsq_linear_fwd", lib().lsq_linear_fwd(
             x.data_ptr(), m, _ptr(w), _ptr(scale), d_out, d_in, _ptr(bias), a, _ptr(residual), w_hat.data_ptr(),
             _ptr(z), y.data_ptr(), ydt, wp, wb, _stream(x)))
@@ -478,11 +513,11 @@ def lsq_linear_bwd(x: torch.Tensor, w_hat: torch.Tensor, grad_y: torch.Tensor, *
         _need(z, "z", torch.bfloat16, (m, d_out), x.device)
     if not (with_x or with_w or with_bias):
         raise ValueError("no gradient asked for")
-    with torch.cuda.device(x.device):
+    with _OnDevice(x.device):
         gx = torch.empty((m, d_in), dtype=torch.bfloat16, device=x.device) if with_x else None
         gw = torch.empty((d_out, d_in), dtype=torch.float32, device=x.device) if with_w else None
         gb = torch.empty(d_out, dtype=torch.float32, device=x.device) if with_bias else None
-        wp, wb, _keep = _workspace("lsq_linear_bwd_workspace_size", (m, d_out, d_in, gdt, a), x.device, workspace)
+        wp, wb, _keep = _scratch("lsq_linear_bwd_workspace_size", (m, d_out, d_in, gdt, a), x.device, workspace)
         check("lsq_linear_bwd", lib().lsq_linear_bwd(
             x.data_ptr(), m, w_hat.data_ptr(), d_out, d_in, grad_y.data_ptr(), gdt, a, _ptr(z) if a != 0 else None,
             _ptr(gx), _ptr(gw), _ptr(gb), wp, wb, _stream(x)))
@@ -504,12 +539,12 @@ def w4a16_linear(x: torch.Tensor, packed: torch.Tensor, scale_f16: torch.Tensor,
     _need(scale_f16, "scale_f16", torch.float16, (d_out, d_in // W4Q_GROUP), x.device)
     a, ydt = _act(act), _dtype_code(out_dtype, "out_dtype")
     _epilogue(m, d_out, out_dtype, x.device, bias, residual)
-    with torch.cuda.device(x.device):
+    with _OnDevice(x.device):
         y = _out(out, "y", (m, d_out), out_dtype, x.device)
         if out is not None:
             _no_overlap((((y, "out"), (t, n)) for t, n in ((x, "x"), (packed, "packed"), (scale_f16, "scale_f16"))))
-        query = "w4a16_gemm_dq_workspace_size" if dequant_bf16 else "w4a16_gemm_workspace_size"
-        wp, wb, _keep = _workspace(query, (m, d_out, d_in), x.device, workspace)
+        wp, wb, _keep = _scratch("w4a16_linear_workspace_size", (m, d_out, d_in, 1 if dequant_bf16 else 0), x.device,
+                                 workspace)
         check("w4a16_linear", lib().w4a16_linear(
             x.data_ptr(), m, packed.data_ptr(), scale_f16.data_ptr(), d_out, d_in, _ptr(bias), a, _ptr(residual),
             y.data_ptr(), ydt, 1 if dequant_bf16 else 0, wp, wb, _stream(x)))
@@ -538,11 +573,11 @@ def newton_schulz(g: torch.Tensor, *, steps: int = 5, coeffs=NS_COEFFS, eps: flo
     o = _dtype_code(odt, "out_dtype")
     if len(coeffs) != 3:
         raise ValueError("coeffs must be (a, b, c)")
-    with torch.cuda.device(g.device):
+    with _OnDevice(g.device):
         y = _out(out, "out", tuple(g.shape), odt, g.device)
         if out is not None and not (y.data_ptr() == g.data_ptr() and y.dtype == g.dtype):
             _no_overlap((((y, "out"), (g, "g")),))
-        wp, wb, _keep = _workspace("newton_schulz_workspace_size", (b, r, c), g.device, workspace)
+        wp, wb, _keep = _scratch("newton_schulz_workspace_size", (b, r, c), g.device, workspace)
         check("newton_schulz", lib().newton_schulz(
             g.data_ptr(), gdt, b, r, c, int(steps), (ctypes.c_float * 3)(*coeffs), float(eps), y.data_ptr(), o, wp, wb,
             _stream(g)))
@@ -568,8 +603,8 @@ def muon_step(w: torch.Tensor, grad: torch.Tensor, m: torch.Tensor, *, lr: float
         update_scale = max(1.0, r / max(c, 1)) ** 0.5
     hp = MuonParams(lr, momentum, weight_decay, update_scale, (ctypes.c_float * 3)(*coeffs), 1 if nesterov else 0,
                     int(steps), float(eps))
-    with torch.cuda.device(w.device):
-        wp, wb, _keep = _workspace("newton_schulz_workspace_size", (b, r, c), w.device, workspace)
+    with _OnDevice(w.device):
+        wp, wb, _keep = _scratch("newton_schulz_workspace_size", (b, r, c), w.device, workspace)
         check("muon_step", lib().muon_step(w.data_ptr(), grad.data_ptr(), m.data_ptr(), b, r, c, ctypes.byref(hp), wp,
                                            wb, _stream(w)))
 
