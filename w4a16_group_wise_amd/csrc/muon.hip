@@ -24,6 +24,7 @@
 // for Y = X^T: A = Y^T Y, Y <- a Y + Y B (B is symmetric).  The products read operands along or across
 // their rows, so nothing is transposed in memory.
 #include "epilogue.hpp"
+#include "muon.hpp"
 #include "nt_gemm.hpp"
 
 namespace w4q {
@@ -184,19 +185,6 @@ struct EpiLast {
 // --------------------------------------------------------------- norm, momentum, first split
 constexpr int kPartMax = 512;    // partial sums of one matrix
 constexpr int kPerPart = 8192;   // elements of one partial sum at least
-
-struct Source {
-  const void* g;     // gradient, fp32 (dtype 0) or bf16 (1)
-  int dtype;
-  float* m;          // momentum buffer or null (newton_schulz)
-  float mu;
-  int nesterov;
-};
-
-__device__ __forceinline__ float grad_at(const Source& s, int64_t i) {
-  return s.dtype == 0 ? static_cast<const float*>(s.g)[i]
-                      : __builtin_bit_cast(float, static_cast<uint32_t>(static_cast<const uint16_t*>(s.g)[i]) << 16);
-}
 
 // Where a matrix's elements start on a 16-byte boundary (vec), values are taken four at a time.
 __device__ __forceinline__ void grad4(const Source& s, int64_t i, float (&g)[4]) {
@@ -386,13 +374,17 @@ using namespace w4q;
 
 bool w4q_ns_fits(int64_t batch, int64_t rows, int64_t cols) {
   if (batch > 65535 || rows > 131072 || cols > 131072) return false;
+  if (w4q_thin(rows, cols)) return true;
   const NsLayout l = ns_layout(batch, rows, cols);
   for (const NtPlan* p : {&l.gram, &l.poly, &l.upd})
     if (p->total > 0x3FFFFFFF) return false;
   return true;
 }
 
-size_t w4q_ns_workspace(int64_t batch, int64_t rows, int64_t cols) { return ns_layout(batch, rows, cols).total; }
+size_t w4q_ns_workspace(int64_t batch, int64_t rows, int64_t cols) {
+  if (w4q_thin(rows, cols)) return w4q_thin_workspace(batch, rows, cols);
+  return ns_layout(batch, rows, cols).total;
+}
 
 // The largest singular value that can occur before each step, from 1 at the start: the extremes of
 // p(s) = a s + b s^3 + c s^5 on [0, M] are at M and where p' = 0.  false where X, A = X X^T or
@@ -435,6 +427,11 @@ bool w4q_ns_coeffs_ok(int steps, double a, double b, double c) {
 int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64_t cols, int steps, float a, float b,
                   float c, double eps, void* out, int out_dtype, float* m, float mu, int nesterov, float* w, float lr,
                   float scale, float wd, void* ws, hipStream_t s) {
+  const Source src = {g, g_dtype, m, mu, nesterov};
+  if (w4q_thin(rows, cols)) {
+    const ThinOut o = {out, out_dtype, w, lr, scale, wd};
+    return w4q_launch_ns_thin(src, batch, rows, cols, steps, a, b, c, eps, o, ws, s);
+  }
   const NsLayout l = ns_layout(batch, rows, cols);
   uint8_t* base = static_cast<uint8_t*>(ws);
   double* sums = reinterpret_cast<double*>(base + l.sums);
@@ -447,7 +444,6 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
   const int n = static_cast<int>(l.n), np = static_cast<int>(l.np);
 
   auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-  const Source src = {g, g_dtype, m, mu, nesterov};
   const bool vec = cols % 8 == 0 && at16(g) && (m == nullptr || at16(m));
   hipLaunchKernelGGL(norm_kernel, dim3(static_cast<unsigned>(l.parts), static_cast<unsigned>(batch)), dim3(256), 0, s, src,
                      rows * cols, l.parts, vec ? 1 : 0, sums);
