@@ -74,12 +74,27 @@ struct EpiLinear {
     }
     store8(y, o, y_dtype, v);
   }
-  __device__ __forceinline__ float load1(const NtArgs& g, int, int row, int col) const {
-    if (ep.res == nullptr || row >= g.M || col >= g.N) return 0.0f;
-    const int64_t o = static_cast<int64_t>(row) * g.N + col;
-    return y_dtype == 0 ? static_cast<const float*>(ep.res)[o] : bf16_val(static_cast<const uint16_t*>(ep.res)[o]);
+  // (addresses past the matrix are clamped rather than branched over, so that the loads overlap)
+  __device__ __forceinline__ void load_rows(const NtArgs& g, int, int row, int col, float (&r)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = 0.0f;
+    if (ep.res == nullptr) return;
+    int64_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e] = static_cast<int64_t>(row + e < g.M ? row + e : g.M - 1) * g.N + (col < g.N ? col : 0);
+    if (y_dtype == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = static_cast<const float*>(ep.res)[o[e]];
+    } else {
+      uint16_t h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = static_cast<const uint16_t*>(ep.res)[o[e]];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = bf16_val(h[e]);
+    }
   }
-  __device__ __forceinline__ void store1(const NtArgs& g, int, int row, int col, float (&v)[8], const float (&r)[8]) const {
+  __device__ __forceinline__ void store_rows(const NtArgs& g, int, int row, int col, float (&v)[8], const float (&r)[8]) const {
     const int64_t o = static_cast<int64_t>(row) * g.N + col;
     const float bv = ep.bias != nullptr ? ep.bias[col] : 0.0f;
 #pragma unroll
@@ -90,7 +105,7 @@ struct EpiLinear {
     activate(v);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (row + e < g.M) w4q::store1(y, o + static_cast<int64_t>(e) * g.N, y_dtype, v[e] + r[e]);
+      if (row + e < g.M) store1(y, o + static_cast<int64_t>(e) * g.N, y_dtype, v[e] + r[e]);
   }
   template <int kAct>
   static __device__ __forceinline__ void act8(float (&v)[8]) {
@@ -120,12 +135,12 @@ struct EpiGrad {
     for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], p.e);
     store8(out, static_cast<int64_t>(row) * g.N + col, out_dtype, v);
   }
-  __device__ __forceinline__ float load1(const NtArgs&, int, int, int) const { return 0.0f; }
-  __device__ __forceinline__ void store1(const NtArgs& g, int, int row, int col, float (&v)[8], const float (&)[8]) const {
+  __device__ __forceinline__ void load_rows(const NtArgs&, int, int, int, float (&)[8]) const {}
+  __device__ __forceinline__ void store_rows(const NtArgs& g, int, int row, int col, float (&v)[8], const float (&)[8]) const {
     const int x = exponent();
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (row + e < g.M) w4q::store1(out, static_cast<int64_t>(row + e) * g.N + col, out_dtype, __builtin_ldexpf(v[e], x));
+      if (row + e < g.M) store1(out, static_cast<int64_t>(row + e) * g.N + col, out_dtype, __builtin_ldexpf(v[e], x));
   }
 };
 

@@ -99,8 +99,8 @@ struct EpiSplit {
   Split o;
 
   __device__ __forceinline__ bool whole() const { return true; }
-  __device__ __forceinline__ float load1(const NtArgs&, int, int, int) const { return 0.0f; }
-  __device__ __forceinline__ void store1(const NtArgs&, int, int, int, const float (&)[8], const float (&)[8]) const {}
+  __device__ __forceinline__ void load_rows(const NtArgs&, int, int, int, float (&)[8]) const {}
+  __device__ __forceinline__ void store_rows(const NtArgs&, int, int, int, const float (&)[8], const float (&)[8]) const {}
   __device__ __forceinline__ Pre load(const NtArgs& g, int batch, int row, int col) const {
     Pre p = {};
     if (c.p != nullptr && row < g.M && col < c.ld) p = load_pair(c, batch, row, col);
@@ -159,25 +159,38 @@ struct EpiLast {
       store8(out, o, out_dtype, v);
     }
   }
-  __device__ __forceinline__ float load1(const NtArgs& g, int batch, int row, int col) const {
-    if (row >= g.M || col >= g.N) return 0.0f;
-    const uint16_t* q = x.p + x.at(batch, row, col);
-    return f16_bits_to_f32(q[0]) + f16_bits_to_f32(q[32]);
-  }
-  __device__ __forceinline__ void store1(const NtArgs& g, int batch, int row, int col, const float (&v)[8],
-                                         const float (&t)[8]) const {
-    const int64_t o = (static_cast<int64_t>(batch) * g.M + row) * g.N + col;
-    float wv[8];
+  // (addresses past the matrix are clamped rather than branched over, so that the loads overlap)
+  __device__ __forceinline__ void load_rows(const NtArgs& g, int batch, int row, int col, float (&t)[8]) const {
+    uint16_t h[8], l[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) wv[e] = w != nullptr && row + e < g.M ? w[o + static_cast<int64_t>(e) * g.N] : 0.0f;
+    for (int e = 0; e < 8; ++e) {
+      const uint16_t* q = x.p + x.at(batch, row + e < g.M ? row + e : g.M - 1, col < x.ld ? col : 0);
+      h[e] = q[0];
+      l[e] = q[32];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = f16_bits_to_f32(h[e]) + f16_bits_to_f32(l[e]);
+  }
+  __device__ __forceinline__ void store_rows(const NtArgs& g, int batch, int row, int col, const float (&v)[8],
+                                             const float (&t)[8]) const {
+    const int64_t o = (static_cast<int64_t>(batch) * g.M + row) * g.N + col;
+    float u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = __builtin_fmaf(alpha, t[e], beta * v[e]) * kSplitInv;
+    if (w != nullptr) {
+      float wv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wv[e] = w[o + (row + e < g.M ? static_cast<int64_t>(e) * g.N : 0)];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = wv[e] - lr * (scale * u[e] + wd * wv[e]);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (row + e >= g.M) continue;
-      const float u = __builtin_fmaf(alpha, t[e], beta * v[e]) * kSplitInv;
       if (w != nullptr)
-        w[o + static_cast<int64_t>(e) * g.N] = wv[e] - lr * (scale * u + wd * wv[e]);
+        w[o + static_cast<int64_t>(e) * g.N] = u[e];
       else
-        w4q::store1(out, o + static_cast<int64_t>(e) * g.N, out_dtype, u);
+        store1(out, o + static_cast<int64_t>(e) * g.N, out_dtype, u[e]);
     }
   }
 };

@@ -219,8 +219,8 @@ __device__ __forceinline__ int64_t nt_part_off(int w, int blk, int q, int lane) 
 //   void store(g, batch, row, col, v[8], pre)        writes the outputs; leaves in v what a mirrored
 //                                                    store shall write
 //   bool whole()                                     false: rows are not multiples of 16 bytes, and
-//   float load1(g, batch, row, col)                  the epilogue runs on 8 rows of one column
-//   void store1(g, batch, row, col, v[8], x[8])      (x: load1 of each row)
+//   void load_rows(g, batch, row, col, x[8])         the epilogue runs on 8 rows of one column
+//   void store_rows(g, batch, row, col, v[8], x[8])
 //   kMirror, void store_t(g, batch, col, row, v[8])  symmetric results: 8 rows of one column
 template <class C>
 struct NtStrip {
@@ -256,18 +256,18 @@ __device__ __forceinline__ void nt_strip_store(const NtArgs& g, const Epi& epi, 
   if (!epi.whole()) {
     // rows that are not multiples of 16 bytes: a lane has one column and 8 rows at a time, so that
     // a wavefront's accesses of a row are still consecutive
-    constexpr int kHalves = 64 / C::WN;  // row groups side by side
-    const int col = col0 + lane % C::WN;
-#pragma unroll 1
-    for (int i = 0; i < 4 / kHalves; ++i) {
-      const int rl = 8 * (i * kHalves + lane / C::WN);
-      float v[8], x[8];
+    constexpr int kGroups = 4 * C::WN / 64;  // groups of 8 rows a lane has
+    const int c = lane % C::WN, r0 = lane / C::WN * (8 * kGroups);
+    // all that is read of the strip in flight at once (16 us of a 1531 x 2050 residual otherwise)
+    float x[kGroups][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = buf[(rl + e) * C::kPitch + lane % C::WN];
-        x[e] = epi.load1(g, batch, row0 + rl + e, col);
-      }
-      if (col < g.N) epi.store1(g, batch, row0 + rl, col, v, x);
+    for (int i = 0; i < kGroups; ++i) epi.load_rows(g, batch, row0 + r0 + 8 * i, col0 + c, x[i]);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = buf[(r0 + 8 * i + e) * C::kPitch + c];
+      if (col0 + c < g.N) epi.store_rows(g, batch, row0 + r0 + 8 * i, col0 + c, v, x[i]);
     }
     asm volatile("" ::: "memory");
     return;
