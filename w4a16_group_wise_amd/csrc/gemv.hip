@@ -259,7 +259,7 @@ struct MmaBatch {
   uint32_t s1[kMmaBatch][kMmaTiles];   // one scale per group (2-byte path)
 };
 
-// kMmaTiles: 16-row tiles of W per workgroup (1 or 2); kWaves: wavefronts per workgroup (8, or
+// kMmaTiles: 16-row tiles of W per workgroup (1 to 3); kWaves: wavefronts per workgroup (8, or
 // 16 for long rows, where each still gets two batches or more)
 template <bool kVecScales, int kMmaTiles, int kWaves = kMmaWaves, bool kEpi = false>
 __global__ __launch_bounds__(kWaves * 64) void gemv_mma_kernel(const uint16_t* __restrict__ x, int m_rows,
@@ -873,10 +873,14 @@ namespace {
 template <bool kEpi>
 int launch_mma(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16, int64_t d_out, int64_t d_in,
                void* y, int y_dtype, hipStream_t s, const W4Epilogue& ep) {
-  const int tiles = d_out < 8192 ? 1 : 2;
+  const bool vec = (d_in / kGroup) % kMmaBatch == 0;
+  // With an epilogue, three tiles per workgroup where two would leave more than one workgroup to some
+  // of the 256 compute units and three do not (8192 < d_out <= 12288; measured for 12288x4096, two
+  // and three tiles: 14.8 and 13.3 us at M = 2, 16.7 and 14.7 at M = 13; 12288x8192: 25.6 and 23.2.
+  // Past that range three lose: 14336x4096 15.8 and 24.1).
+  const int tiles = d_out < 8192 ? 1 : kEpi && vec && d_out > 8192 && d_out <= 12288 ? 3 : 2;
   const int64_t blocks = (d_out + 16 * tiles - 1) / (16 * tiles);
   if (blocks > 0x7FFFFFFF) return W4Q_EUNSUPPORTED;
-  const bool vec = (d_in / kGroup) % kMmaBatch == 0;
   auto run = [&](auto kernel, int waves) {
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(waves * 64), 0, s, x, static_cast<int>(m), packed,
                        s16, d_out, d_in, y, y_dtype, ep);
@@ -890,6 +894,8 @@ int launch_mma(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16
       run(gemv_mma_kernel<true, 1, 16, kEpi>, 16);
     else
       run(gemv_mma_kernel<false, 1, 16, kEpi>, 16);
+  } else if (tiles == 3) {
+    if constexpr (kEpi) run(gemv_mma_kernel<true, 3, kMmaWaves, kEpi>, kMmaWaves);
   } else if (vec && tiles == 2) {
     run(gemv_mma_kernel<true, 2, kMmaWaves, kEpi>, kMmaWaves);
   } else if (vec) {
