@@ -43,8 +43,8 @@ enum w4q_act { W4Q_ACT_NONE = 0, W4Q_ACT_RELU = 1, W4Q_ACT_GELU = 2, W4Q_ACT_SIL
  *   y         [m][d_out], fp32 (y_dtype 0) or bf16 RNE (y_dtype 1).
  *   workspace NULL with 0 bytes, or 256-B aligned scratch; with less than the query's size no
  *             output tile is split over workgroups (same arithmetic up to the summation order).
- *   Limits: m, d_out < 2^30, d_in <= 2^21, and at most 2^30 steps of 32 k over all output tiles
- *   (W4Q_EUNSUPPORTED).
+ *   Limits: m, d_out < 2^30, d_in <= 2^21, at most 2^30 steps of 32 k over all 64 x 64 output
+ *   tiles, and at most 2^24 - 16 of the tiles (W4Q_EUNSUPPORTED).
  */
 int lsq_linear_fwd(const uint16_t* x, int64_t m, const float* w, const float* scale, int64_t d_out,
                    int64_t d_in, const float* bias, int act, const void* residual, uint16_t* w_hat,
@@ -109,8 +109,8 @@ int w4a16_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int w_mo
  *   Operands of the products are held in 22 bits and summed in fp32: the error is that of fp32
  *   products.
  *   workspace  newton_schulz_workspace_size bytes, 256-B aligned (W4Q_EINVAL if smaller or NULL).
- *   Limits: 1 <= rows, cols <= 131072, batch <= 65535, and at most 2^30 steps of 32 k over all
- *   output tiles of a product (W4Q_EUNSUPPORTED).
+ *   Limits: 1 <= rows, cols <= 131072, batch <= 65535, at most 2^30 steps of 32 k over all
+ *   output tiles of a product and at most 2^24 - 16 tiles (W4Q_EUNSUPPORTED).
  */
 int newton_schulz(const void* g, int g_dtype, int64_t batch, int64_t rows, int64_t cols, int steps,
                   const float* coeffs, double eps, void* out, int out_dtype, void* workspace,

@@ -39,6 +39,7 @@ def fwd(**kw):
     (dict(act=4), INV), (dict(act=-1), INV), (dict(ydt=2), INV), (dict(m=0), SHAPE), (dict(d_out=0), SHAPE),
     (dict(d_in=0), SHAPE), (dict(d_in=48), SHAPE), (dict(m=1 << 41), SHAPE), (dict(d_in=32 << 17), UNSUP),
     (dict(m=1 << 30, d_in=32, d_out=1), UNSUP), (dict(m=1 << 24, d_out=1 << 14, d_in=1 << 14), UNSUP),
+    (dict(m=(1 << 30) - 1, d_in=32, d_out=1), UNSUP), (dict(m=1 << 29, d_in=32, d_out=128), UNSUP),
     (dict(x=A + 2), ALIGN), (dict(w=A + 4), ALIGN), (dict(w_hat=A + 8), ALIGN), (dict(scale=A + 2), ALIGN),
     (dict(bias=A + 1), ALIGN), (dict(y=B), ALIGN), (dict(ydt=0, y=A + 2), ALIGN), (dict(res=B), ALIGN),
     (dict(ydt=0, res=A + 2), ALIGN), (dict(z=B), ALIGN), (dict(ws=None, wb=256), INV), (dict(ws=A + 128, wb=256), ALIGN)])
@@ -126,6 +127,9 @@ def test_workspace_queries():
     assert L.lsq_linear_fwd_workspace_size(0, 8, 64, p) == SHAPE
     assert L.lsq_linear_bwd_workspace_size(4, 8, 48, 1, 0, p) == SHAPE
     assert L.lsq_linear_bwd_workspace_size(4, 8, 64, 2, 0, p) == INV
+    assert L.w4a16_linear_workspace_size(4, 8, 64, 0, None) == INV
+    assert L.w4a16_linear_workspace_size(4, 8, 64, 2, p) == INV
+    assert L.w4a16_linear_workspace_size(4, 8, 65, 0, p) == SHAPE
     assert L.newton_schulz_workspace_size(1, 0, 8, p) == SHAPE
     assert L.newton_schulz_workspace_size(1, 8, 131073, p) == UNSUP
     assert w4q.workspace_size("lsq_linear_fwd", 1, 32, 32) == 0

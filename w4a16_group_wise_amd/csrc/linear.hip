@@ -484,12 +484,11 @@ __global__ __launch_bounds__(256) void dequant_kernel(const u32x4* __restrict__ 
   }
 }
 
-// row lengths whose 256-row tiles stay within 32-bit buffer offsets, and iteration counts of the products
-constexpr int64_t kMaxIterations = 0x3FFFFFFF;
-int64_t most_iterations(int64_t M, int64_t N, int64_t K) { return nt_plan_tile(2, 1, M, N, K, false, 32).total; }
+// row lengths whose 256-row tiles stay within 32-bit buffer offsets, and iteration and thread counts of
+// the products
+bool product_fits(int64_t M, int64_t N, int64_t K) { return nt_fits(nt_plan_tile(2, 1, M, N, K, false, 32)); }
 bool fits(int64_t M, int64_t N, int64_t K) {
-  if (M > 0x3FFFFFFF || N > 0x3FFFFFFF || K > (1 << 21)) return false;
-  return most_iterations(M, N, K) <= kMaxIterations;
+  return M <= 0x3FFFFFFF && N <= 0x3FFFFFFF && K <= (1 << 21) && product_fits(M, N, K);
 }
 
 }  // namespace
@@ -501,7 +500,7 @@ bool w4q_linear_fits(int64_t m, int64_t d_out, int64_t d_in, bool backward) {
   if (!backward) return fits(m, d_out, d_in);
   // one workgroup per 64 rows in the pass over dz; 32 rows of an operand within 32-bit buffer offsets
   if ((m + kDzRows - 1) / kDzRows > 65535 || d_in > (1 << 21)) return false;
-  return fits(m, d_in, up32(d_out)) && most_iterations(d_out, d_in, m) <= kMaxIterations;
+  return fits(m, d_in, up32(d_out)) && product_fits(d_out, d_in, m);
 }
 
 size_t w4q_linear_fwd_workspace(int64_t m, int64_t d_out, int64_t d_in) { return lin_plan(m, d_out, d_in, 1, true).ws; }

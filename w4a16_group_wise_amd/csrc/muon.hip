@@ -387,16 +387,16 @@ using namespace w4q;
 
 bool w4q_ns_fits(int64_t batch, int64_t rows, int64_t cols) {
   if (batch > 65535 || rows > 131072 || cols > 131072) return false;
-  if (w4q_thin(rows, cols)) return true;
   const NsLayout l = ns_layout(batch, rows, cols);
-  for (const NtPlan* p : {&l.gram, &l.poly, &l.upd})
-    if (p->total > 0x3FFFFFFF) return false;
-  return true;
+  return nt_fits(l.gram) && nt_fits(l.poly) && nt_fits(l.upd);
 }
 
 size_t w4q_ns_workspace(int64_t batch, int64_t rows, int64_t cols) {
-  if (w4q_thin(rows, cols)) return w4q_thin_workspace(batch, rows, cols);
-  return ns_layout(batch, rows, cols).total;
+  // (short sides take either way, by the steps and coefficients of the call)
+  const size_t products = ns_layout(batch, rows, cols).total;
+  if (!w4q_thin(rows, cols)) return products;
+  const size_t thin = w4q_thin_workspace(batch, rows, cols);
+  return thin > products ? thin : products;
 }
 
 // The largest singular value that can occur before each step, from 1 at the start: the extremes of
@@ -441,7 +441,7 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
                   float c, double eps, void* out, int out_dtype, float* m, float mu, int nesterov, float* w, float lr,
                   float scale, float wd, void* ws, hipStream_t s) {
   const Source src = {g, g_dtype, m, mu, nesterov};
-  if (w4q_thin(rows, cols)) {
+  if (w4q_thin(rows, cols) && w4q_thin_steps_ok(steps, a)) {
     const ThinOut o = {out, out_dtype, w, lr, scale, wd};
     return w4q_launch_ns_thin(src, batch, rows, cols, steps, a, b, c, eps, o, ws, s);
   }

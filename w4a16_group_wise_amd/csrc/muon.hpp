@@ -35,6 +35,7 @@ struct ThinOut {
 }  // namespace w4q
 
 bool w4q_thin(int64_t rows, int64_t cols);
+bool w4q_thin_steps_ok(int steps, double a);
 size_t w4q_thin_workspace(int64_t batch, int64_t rows, int64_t cols);
 int w4q_launch_ns_thin(const w4q::Source& src, int64_t batch, int64_t rows, int64_t cols, int steps, float a, float b,
                        float c, double eps, const w4q::ThinOut& o, void* ws, hipStream_t s);

@@ -1,5 +1,5 @@
-// muon_thin.hip -- the orthogonalised update for matrices with a short side n <= 64 (muon.hip has the
-// others): three launches instead of two and three per step.
+// muon_thin.hip -- the orthogonalised update for matrices with a short side n <= 64 and few steps
+// (muon.hip has the others): three launches instead of two and three per step.
 //
 // Every iterate is a polynomial in A = X0 X0^T applied to X0, and those polynomials commute, so the
 // steps can be taken on n x n matrices alone (X is n x k, k >= n):
@@ -318,6 +318,16 @@ int launch_thin(const ThinLayout& l, const Source& src, int64_t batch, int64_t r
 using namespace w4q;
 
 bool w4q_thin(int64_t rows, int64_t cols) { return (rows < cols ? rows : cols) <= kThinMax; }
+
+// Where X has (nearly) lost rank, roundings leave A eigenvalues of either sign near zero, about 2^-50 of its
+// trace, and every step multiplies those by up to a^2: a negative one that reaches the size of the others
+// runs away, as no singular value of X can.  So steps that could bring it to 2^-24 are taken on X itself
+// (muon.hip); with the published coefficients that is from 8 steps on.
+bool w4q_thin_steps_ok(int steps, double a) {
+  double grown = 1.0;
+  for (int i = 0; i < steps; ++i) grown *= a * a;
+  return grown <= 67108864.0;  // 2^26
+}
 
 size_t w4q_thin_workspace(int64_t batch, int64_t rows, int64_t cols) { return thin_layout(batch, rows, cols).total; }
 

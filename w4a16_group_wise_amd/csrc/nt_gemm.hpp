@@ -514,7 +514,7 @@ __global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi 
 // For products too small to fill the device with tiles of 64: 32x32 tiles, the stages of a tile dealt
 // to the 8 wavefronts of a workgroup, each with LDS buffers of its own (no barrier until the end, all
 // loads of a short sum in flight at once), the wavefronts' sums added in LDS in a fixed order.  256 x 512
-// Newton-Schulz products: 8 us each on 64x64 tiles, LDSUS us here.
+// Newton-Schulz products: 8 us each on 64x64 tiles, 5.5 us here.
 template <int PA_, int PB_, bool F16_, bool AT_, bool BT_, bool LOLO_ = false>
 struct NtTinyCfg {
   static constexpr int BM = 32, BN = 32, WM = 32, WN = 32, PA = PA_, PB = PB_;
@@ -692,6 +692,10 @@ inline NtPlan nt_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, 
   return best;
 }
 
+// Iterations in an int with room for sums of two, and workgroups whose threads (256, or 512 on tiles of
+// 256 and 32, of which a plan never takes more than half as many as tiles of 64) count below 2^32.
+inline bool nt_fits(const NtPlan& p) { return p.total <= 0x3FFFFFFF && p.nblk <= 0xFFFFF0; }
+
 // one product: fills in the plan, launches the product and, where tiles were split, the fixup
 inline void nt_fill(NtArgs& g, const NtPlan& p, int tri, void* ws) {
   g.tm = static_cast<int>(p.tm);
@@ -708,7 +712,7 @@ inline void nt_fill(NtArgs& g, const NtPlan& p, int tri, void* ws) {
 
 template <class C, class Epi>
 int nt_launch_tiny(NtArgs g, const NtPlan& p, int tri, const Epi& epi, hipStream_t s) {
-  if (p.total > 0x3FFFFFFF) return W4Q_EUNSUPPORTED;
+  if (!nt_fits(p)) return W4Q_EUNSUPPORTED;
   nt_fill(g, p, tri, nullptr);
   hipLaunchKernelGGL((nt_tiny_kernel<C, Epi>), dim3(static_cast<unsigned>(8 * g.per_xcd)), dim3(C::kThreads), 0, s, g, epi);
   return w4q_launch_status();
@@ -716,7 +720,7 @@ int nt_launch_tiny(NtArgs g, const NtPlan& p, int tri, const Epi& epi, hipStream
 
 template <class C, class Epi>
 int nt_launch(NtArgs g, const NtPlan& p, int tri, const Epi& epi, void* ws, hipStream_t s) {
-  if (p.total > 0x3FFFFFFF) return W4Q_EUNSUPPORTED;
+  if (!nt_fits(p)) return W4Q_EUNSUPPORTED;
   nt_fill(g, p, tri, ws);
   hipLaunchKernelGGL((nt_kernel<C, Epi>), dim3(static_cast<unsigned>(8 * g.per_xcd)), dim3(C::kThreads), 0, s, g, epi);
   int rc = w4q_launch_status();
