@@ -216,28 +216,31 @@ __device__ __forceinline__ int scale_exp(const float* __restrict__ parts) {
 }
 
 // x and W as fp16 times the power of two of their maxima (exact: 8 significant bits), whose
-// exponents go to exps[1] and exps[2].  blockIdx.y: which.  HBM bound: 4 B per value.
+// exponents go to exps[1] and exps[2].  HBM bound: 4 B per value.
 struct ConvertArgs {
   const uint16_t* src[2];
   uint16_t* dst[2];
-  int64_t n8[2];  // eights of values; 0: not wanted
+  int64_t n8[2];   // eights of values
+  int blocks[2];   // workgroups that convert it; 0: not wanted
+  int* exps;
 };
-__global__ __launch_bounds__(256) void convert_kernel(const ConvertArgs a, const float* __restrict__ parts, int* __restrict__ exps) {
-  const int t = blockIdx.y;
-  if (a.n8[t] == 0) return;
+__device__ __forceinline__ void convert_part(const ConvertArgs& a, int t, int block, const float* __restrict__ parts) {
+  const int64_t first = static_cast<int64_t>(block) * 256 + threadIdx.x;
+  const u32x4 ahead = first < a.n8[t] ? reinterpret_cast<const u32x4*>(a.src[t])[first] : u32x4{0, 0, 0, 0};
   const int e = scale_exp(parts + (t + 1) * kAmaxBlocks);
-  if (blockIdx.x == 0 && threadIdx.x == 0) exps[t + 1] = e;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-#pragma unroll 2
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < a.n8[t]; i += step) {
-    const u32x4 v = reinterpret_cast<const u32x4*>(a.src[t])[i];
+  if (block == 0 && threadIdx.x == 0) a.exps[t + 1] = e;
+  const int64_t step = static_cast<int64_t>(a.blocks[t]) * 256;
+  auto put = [&](int64_t i, const u32x4& v) {
     u32x4 o;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       o[j] = f32_to_f16_bits(__builtin_ldexpf(bf16_lo(v[j]), e)) |
              (static_cast<uint32_t>(f32_to_f16_bits(__builtin_ldexpf(bf16_hi(v[j]), e))) << 16);
     reinterpret_cast<u32x4*>(a.dst[t])[i] = o;
-  }
+  };
+  if (first < a.n8[t]) put(first, ahead);
+#pragma unroll 2
+  for (int64_t i = first + step; i < a.n8[t]; i += step) put(i, reinterpret_cast<const u32x4*>(a.src[t])[i]);
 }
 
 // dz = dy act'(z), rows padded to np values with zeros: as two fp16 parts of dz 2^e (kSplit), or (no
@@ -255,6 +258,7 @@ struct DzArgs {
   float* bsum;        // [ceil(m / 64)][n] or null
   const float* parts;
   int* exp_out;
+  int cols, blocks;   // workgroups along a row, and of the whole pass; those behind them convert x and W
 };
 // the fp16 parts of v 2^e; an infinite v stays infinite (its rest is NaN)
 __device__ __forceinline__ void dz_split(float v, int e, uint16_t& h, uint16_t& l) {
@@ -269,16 +273,29 @@ __device__ __forceinline__ void dact8(float (&v)[8], const float (&z)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] *= act_grad(z[j], kAct);
 }
+// the conversion, for a workgroup behind those of the pass over dz (one launch for both)
 template <bool kSplit>
-__global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
+__device__ __forceinline__ bool dz_converts(const DzArgs& a, const ConvertArgs& c) {
+  if constexpr (kSplit) {
+    const int b = static_cast<int>(blockIdx.x) - a.blocks;
+    if (b < 0) return false;
+    b < c.blocks[0] ? convert_part(c, 0, b, a.parts) : convert_part(c, 1, b - c.blocks[0], a.parts);
+    return true;
+  }
+  return false;
+}
+template <bool kSplit>
+__global__ __launch_bounds__(256) void dz_kernel(const DzArgs a, const ConvertArgs c) {
   __shared__ float cs[8][257];
+  if (dz_converts<kSplit>(a, c)) return;
   int e = 0;
   if constexpr (kSplit) {
     e = scale_exp(a.parts);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.exp_out = e;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.exp_out = e;
   }
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + 8 * (threadIdx.x & 31);
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kDzRows + (threadIdx.x >> 5);
+  const int bx = static_cast<int>(blockIdx.x) % a.cols, by = static_cast<int>(blockIdx.x) / a.cols;
+  const int64_t col = static_cast<int64_t>(bx) * 256 + 8 * (threadIdx.x & 31);
+  const int64_t r0 = static_cast<int64_t>(by) * kDzRows + (threadIdx.x >> 5);
   float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 2
   for (int i = 0; i < kDzRows / 8; ++i) {
@@ -327,38 +344,56 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) cs[threadIdx.x >> 5][8 * (threadIdx.x & 31) + j] = sum[j];
   __syncthreads();
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (c >= a.n) return;
+  const int64_t oc = static_cast<int64_t>(bx) * 256 + threadIdx.x;
+  if (oc >= a.n) return;
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) s += cs[j][threadIdx.x];
-  a.bsum[blockIdx.y * a.n + c] = s;
+  a.bsum[by * a.n + oc] = s;
 }
 
 // The same where rows are not multiples of 16 bytes: a thread has one column, so that accesses of a row
 // are consecutive, and 16 rows at a time; 64 columns x 64 rows to a workgroup.
 template <bool kSplit>
-__global__ __launch_bounds__(256) void dz_ragged_kernel(const DzArgs a) {
+__global__ __launch_bounds__(256) void dz_ragged_kernel(const DzArgs a, const ConvertArgs c) {
   __shared__ float cs[4][64];
+  if (dz_converts<kSplit>(a, c)) return;
+  const int bx = static_cast<int>(blockIdx.x) % a.cols, by = static_cast<int>(blockIdx.x) / a.cols;
+  const int64_t col = static_cast<int64_t>(bx) * 64 + (threadIdx.x & 63);
+  const int64_t r0 = static_cast<int64_t>(by) * kDzRows + 16 * (threadIdx.x >> 6);
+  // everything the thread reads, in flight together and while the exponent is found (places past the
+  // matrix read its first value)
+  uint32_t dr[16], zr[16];
+  auto at = [&](int j) { return r0 + j < a.m && col < a.n ? (r0 + j) * a.n + col : 0; };
+  if (a.dy_f32) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) dr[j] = static_cast<const uint32_t*>(a.dy)[at(j)];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) dr[j] = static_cast<const uint16_t*>(a.dy)[at(j)];
+  }
+  if (a.act != W4Q_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) zr[j] = a.z[at(j)];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) zr[j] = 0;
+  }
   int e = 0;
   if constexpr (kSplit) {
     e = scale_exp(a.parts);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.exp_out = e;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.exp_out = e;
   }
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kDzRows + 16 * (threadIdx.x >> 6);
   float sum = 0.0f;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     float v[8], zv[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t row = r0 + 8 * half + j;
-      const bool in = row < a.m && col < a.n;
-      const int64_t o = in ? row * a.n + col : 0;
-      const float d = a.dy_f32 ? static_cast<const float*>(a.dy)[o] : bf16_val(static_cast<const uint16_t*>(a.dy)[o]);
-      v[j] = in ? d : 0.0f;
-      zv[j] = a.act != W4Q_ACT_NONE ? bf16_val(a.z[o]) : 0.0f;
+      const bool in = r0 + 8 * half + j < a.m && col < a.n;
+      const uint32_t d = dr[8 * half + j];
+      v[j] = in ? __builtin_bit_cast(float, a.dy_f32 ? d : d << 16) : 0.0f;
+      zv[j] = __builtin_bit_cast(float, zr[8 * half + j] << 16);
     }
     switch (a.act) {
       case W4Q_ACT_RELU: dact8<W4Q_ACT_RELU>(v, zv); break;
@@ -390,7 +425,7 @@ __global__ __launch_bounds__(256) void dz_ragged_kernel(const DzArgs a) {
   cs[threadIdx.x >> 6][threadIdx.x & 63] = sum;
   __syncthreads();
   if (threadIdx.x < 64 && col < a.n)
-    a.bsum[blockIdx.y * a.n + col] = (cs[0][threadIdx.x] + cs[1][threadIdx.x]) + (cs[2][threadIdx.x] + cs[3][threadIdx.x]);
+    a.bsum[by * a.n + col] = (cs[0][threadIdx.x] + cs[1][threadIdx.x]) + (cs[2][threadIdx.x] + cs[3][threadIdx.x]);
 }
 
 // dbias: the tiles' column sums added in row order, in fp64 (one rounding at the end)
@@ -409,6 +444,11 @@ template <int PA, bool F16, bool AT, bool BT>
 using Big = NtCfg<256, 256, 128, 64, PA, 1, F16, AT, BT>;
 template <int PA, bool F16, bool AT, bool BT>
 using Mid = NtCfg<128, 128, 64, 64, PA, 1, F16, AT, BT>;
+// where no compute unit gets two workgroups, eight wavefronts a tile rather than four: two on each SIMD
+// (1531x2050x1056 forward: 38.5 -> 34.3 us; with two workgroups on a compute unit four are better,
+// 2048x4096x4096: 95 and 105 us)
+template <int PA, bool F16, bool AT, bool BT>
+using MidAlone = NtCfg<128, 128, 64, 32, PA, 1, F16, AT, BT>;
 template <int PA, bool F16, bool AT, bool BT>
 using Small = NtCfg<64, 64, 32, 32, PA, 1, F16, AT, BT>;
 
@@ -420,6 +460,7 @@ NtPlan lin_plan(int64_t M, int64_t N, int64_t K, int parts, bool tiny, bool spli
 template <int PA, bool F16, bool AT, bool BT, class Epi>
 int lin_product(const NtArgs& g, const NtPlan& p, const Epi& e, void* ws, hipStream_t s) {
   if (p.kind == 0) return nt_launch<Big<PA, F16, AT, BT>, Epi>(g, p, 0, e, ws, s);
+  if (p.kind == 1 && p.nblk <= kNtCus) return nt_launch<MidAlone<PA, F16, AT, BT>, Epi>(g, p, 0, e, ws, s);
   if (p.kind == 1) return nt_launch<Mid<PA, F16, AT, BT>, Epi>(g, p, 0, e, ws, s);
   if constexpr (!AT && !BT) {
     if (p.kind == 3) return nt_launch_tiny<NtTinyCfg<PA, 1, F16, AT, BT>, Epi>(g, p, 0, e, s);
@@ -498,8 +539,10 @@ using namespace w4q;
 
 bool w4q_linear_fits(int64_t m, int64_t d_out, int64_t d_in, bool backward) {
   if (!backward) return fits(m, d_out, d_in);
-  // one workgroup per 64 rows in the pass over dz; 32 rows of an operand within 32-bit buffer offsets
-  if ((m + kDzRows - 1) / kDzRows > 65535 || d_in > (1 << 21)) return false;
+  // workgroups of the pass over dz and the conversions (64 rows x 64 columns at least); 32 rows of an
+  // operand within 32-bit buffer offsets
+  const int64_t mt = (m + kDzRows - 1) / kDzRows;
+  if (mt > 65535 || d_in > (1 << 21) || d_out > (1 << 21) || mt * ((d_out + 63) / 64) > (1 << 24) - (1 << 13)) return false;
   return fits(m, d_in, up32(d_out)) && product_fits(d_out, d_in, m);
 }
 
@@ -565,18 +608,20 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
     const AmaxArgs a = {{dy, x, w_hat}, {m * d_out, dw != nullptr ? m * d_in : 0, dx != nullptr ? d_out * d_in : 0}, {dy_f32, 0, 0}};
     hipLaunchKernelGGL(amax_kernel, dim3(kAmaxBlocks, 3), dim3(256), 0, s, a, parts);
     if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
-    const ConvertArgs c = {{x, w_hat}, {u16(l.x16), u16(l.w16)}, {dw != nullptr ? m * d_in / 8 : 0, dx != nullptr ? d_out * d_in / 8 : 0}};
-    const int64_t most = (c.n8[0] > c.n8[1] ? c.n8[0] : c.n8[1]) / 512 + 1;
-    hipLaunchKernelGGL(convert_kernel, dim3(static_cast<unsigned>(most < 2048 ? most : 2048), 2), dim3(256), 0, s, c, parts, exps);
-    if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
   }
   const bool need = products && !l.direct;
   if (need || db != nullptr) {
-    const DzArgs a = {dy, dy_f32, z, act, m, d_out, l.np, need && (dx != nullptr || !l.split) ? u16(l.hi) : nullptr,
-                      l.split && dw != nullptr ? u16(l.both) : nullptr, bsum, parts, exps};
     const bool whole = d_out % 8 == 0 && at16(z);
-    const dim3 grid(static_cast<unsigned>(whole ? (l.np + 255) / 256 : (l.np + 63) / 64), static_cast<unsigned>(l.mt));
-    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
+    const int64_t cols = whole ? (l.np + 255) / 256 : (l.np + 63) / 64;
+    const DzArgs a = {dy, dy_f32, z, act, m, d_out, l.np, need && (dx != nullptr || !l.split) ? u16(l.hi) : nullptr,
+                      l.split && dw != nullptr ? u16(l.both) : nullptr, bsum, parts, exps, static_cast<int>(cols),
+                      static_cast<int>(cols * l.mt)};
+    ConvertArgs c = {{x, w_hat}, {u16(l.x16), u16(l.w16)}, {m * d_in / 8, d_out * d_in / 8}, {0, 0}, exps};
+    auto blocks = [](int64_t n8) { return static_cast<int>(n8 / 512 + 1 < 2048 ? n8 / 512 + 1 : 2048); };
+    if (l.split && dw != nullptr) c.blocks[0] = blocks(c.n8[0]);
+    if (l.split && dx != nullptr) c.blocks[1] = blocks(c.n8[1]);
+    const dim3 grid(static_cast<unsigned>(a.blocks + c.blocks[0] + c.blocks[1]));
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, c); };
     if (l.split && need)
       whole ? run(dz_kernel<true>) : run(dz_ragged_kernel<true>);
     else

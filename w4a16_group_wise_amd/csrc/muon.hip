@@ -326,6 +326,8 @@ using Big = NtCfg<256, 256, 128, 64, 2, 2, true, AT, BT>;
 template <bool AT, bool BT>
 using Mid = NtCfg<128, 128, 64, 64, 2, 2, true, AT, BT>;
 template <bool AT, bool BT>
+using MidAlone = NtCfg<128, 128, 64, 32, 2, 2, true, AT, BT>;
+template <bool AT, bool BT>
 using Small = NtCfg<64, 64, 32, 32, 2, 2, true, AT, BT, true>;
 
 NtPlan ns_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri) {
@@ -335,6 +337,7 @@ NtPlan ns_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri) {
 template <bool AT, bool BT, class Epi>
 int ns_product(const NtArgs& g, const NtPlan& p, int tri, const Epi& e, void* ws, hipStream_t s) {
   if (p.kind == 0) return nt_launch<Big<AT, BT>, Epi>(g, p, tri, e, ws, s);
+  if (p.kind == 1 && p.nblk <= kNtCus) return nt_launch<MidAlone<AT, BT>, Epi>(g, p, tri, e, ws, s);
   if (p.kind == 1) return nt_launch<Mid<AT, BT>, Epi>(g, p, tri, e, ws, s);
   if (p.kind == 2) return nt_launch<Small<AT, BT>, Epi>(g, p, tri, e, ws, s);
   return nt_launch_tiny<NtTinyCfg<2, 2, true, AT, BT, true>, Epi>(g, p, tri, e, s);
