@@ -68,7 +68,7 @@ int lsq_linear_fwd_workspace_size(int64_t m, int64_t d_out, int64_t d_in, size_t
  *   dz enters grad_w_hat in 22 bits and grad_x in 11 (with W4Q_ACT_NONE and bf16 grad_y: as it
  *   is), relative to values within 2^-24 of the largest |grad_y|.
  *   workspace  lsq_linear_bwd_workspace_size bytes, 256-B aligned (W4Q_EINVAL if smaller or NULL).
- *   Limits: as for the forward, with m <= 4194240, d_out <= 2^21 and at most 2^24 - 2^13 blocks of
+ *   Limits: as for the forward, with m <= 4194240, d_out <= 2^20 and at most 2^24 - 2^13 blocks of
  *   64 x 64 in dz (W4Q_EUNSUPPORTED).
  */
 int lsq_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, int64_t d_out, int64_t d_in,

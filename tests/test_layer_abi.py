@@ -57,7 +57,7 @@ def bwd(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(x=None), INV), (dict(w_hat=None), INV), (dict(gy=None), INV), (dict(z=None), INV), (dict(act=9), INV),
     (dict(gdt=2), INV), (dict(gx=None, gw=None, gb=None), INV), (dict(m=-1), SHAPE), (dict(d_in=33), SHAPE),
-    (dict(d_out=-3), SHAPE), (dict(m=4194241), UNSUP), (dict(d_in=32 << 17), UNSUP), (dict(d_out=(1 << 21) + 1), UNSUP),
+    (dict(d_out=-3), SHAPE), (dict(m=4194241), UNSUP), (dict(d_in=32 << 17), UNSUP), (dict(d_out=(1 << 20) + 1), UNSUP),
     (dict(m=4194240, d_out=1 << 14, d_in=32), UNSUP), (dict(x=A + 8), ALIGN),
     (dict(w_hat=A + 8), ALIGN), (dict(gy=A + 8), ALIGN), (dict(z=B), ALIGN), (dict(gx=B), ALIGN), (dict(gw=A + 2), ALIGN),
     (dict(gb=A + 2), ALIGN), (dict(ws=None, wb=0), INV), (dict(ws=A + 16), ALIGN), (dict(wb=1024), INV)])

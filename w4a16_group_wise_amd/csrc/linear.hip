@@ -254,7 +254,8 @@ struct DzArgs {
   const uint16_t* z;
   int act;
   int64_t m, n, np;
-  uint16_t *hi, *both;  // null: not wanted
+  uint16_t* out;      // [m][np], or with two parts [m][hi np, lo np]; null (not with parts): not wanted
+  int lo;             // the second part is wanted
   float* bsum;        // [ceil(m / 64)][n] or null
   const float* parts;
   int* exp_out;
@@ -318,8 +319,8 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a, const ConvertAr
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += v[j];
-    if (!kSplit && a.hi == nullptr) continue;
-    const int64_t at = row * a.np + col;
+    if (a.out == nullptr) continue;
+    uint16_t* q = a.out + row * ((kSplit ? 2 : 1) * a.np) + col;
     if constexpr (kSplit) {
       u32x4 h, l;
 #pragma unroll
@@ -330,14 +331,10 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a, const ConvertAr
         h[j] = h0 | (static_cast<uint32_t>(h1) << 16);
         l[j] = l0 | (static_cast<uint32_t>(l1) << 16);
       }
-      if (a.hi != nullptr) *reinterpret_cast<u32x4*>(a.hi + at) = h;
-      if (a.both != nullptr) {  // the split matrix: the parts of 32 columns side by side
-        uint16_t* q = a.both + row * (2 * a.np) + (col >> 5) * 64 + (col & 31);
-        *reinterpret_cast<u32x4*>(q) = h;
-        *reinterpret_cast<u32x4*>(q + 32) = l;
-      }
+      *reinterpret_cast<u32x4*>(q) = h;
+      if (a.lo) *reinterpret_cast<u32x4*>(q + a.np) = l;
     } else {
-      *reinterpret_cast<u32x4*>(a.hi + at) = d0;  // dy as it lies (bf16)
+      *reinterpret_cast<u32x4*>(q) = d0;  // dy as it lies (bf16)
     }
   }
   if (a.bsum == nullptr) return;
@@ -410,14 +407,11 @@ __global__ __launch_bounds__(256) void dz_ragged_kernel(const DzArgs a, const Co
       if constexpr (kSplit) {
         uint16_t h, l;
         dz_split(v[j], e, h, l);
-        if (a.hi != nullptr) a.hi[row * a.np + col] = h;
-        if (a.both != nullptr) {
-          uint16_t* q = a.both + row * (2 * a.np) + (col >> 5) * 64 + (col & 31);
-          q[0] = h;
-          q[32] = l;
-        }
-      } else if (a.hi != nullptr) {
-        a.hi[row * a.np + col] = bf16_bits(v[j]);  // dy itself (bf16): exact
+        uint16_t* q = a.out + row * (2 * a.np) + col;
+        q[0] = h;
+        if (a.lo) q[a.np] = l;
+      } else if (a.out != nullptr) {
+        a.out[row * a.np + col] = bf16_bits(v[j]);  // dy itself (bf16): exact
       }
     }
   }
@@ -477,7 +471,7 @@ struct BwdLayout {
   bool direct;       // the products read dy as it lies
   int64_t np, mt;
   NtPlan px, pw;
-  size_t parts, exps, hi, both, x16, w16, bsum, part, total;
+  size_t parts, exps, dz, x16, w16, bsum, part, total;
 };
 BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   BwdLayout l;
@@ -495,8 +489,7 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   };
   l.parts = take(l.split ? 3 * kAmaxBlocks * sizeof(float) : 0);
   l.exps = take(l.split ? 3 * sizeof(int) : 0);
-  l.hi = take(l.direct ? 0 : size_t(2) * m * l.np);
-  l.both = take(l.split ? size_t(4) * m * l.np : 0);
+  l.dz = take(l.direct ? 0 : size_t(l.split ? 4 : 2) * m * l.np);
   l.x16 = take(l.split ? size_t(2) * m * k : 0);
   l.w16 = take(l.split ? size_t(2) * n * k : 0);
   l.bsum = take(sizeof(float) * l.mt * n);
@@ -542,7 +535,7 @@ bool w4q_linear_fits(int64_t m, int64_t d_out, int64_t d_in, bool backward) {
   // workgroups of the pass over dz and the conversions (64 rows x 64 columns at least); 32 rows of an
   // operand within 32-bit buffer offsets
   const int64_t mt = (m + kDzRows - 1) / kDzRows;
-  if (mt > 65535 || d_in > (1 << 21) || d_out > (1 << 21) || mt * ((d_out + 63) / 64) > (1 << 24) - (1 << 13)) return false;
+  if (mt > 65535 || d_in > (1 << 21) || d_out > (1 << 20) || mt * ((d_out + 63) / 64) > (1 << 24) - (1 << 13)) return false;
   return fits(m, d_in, up32(d_out)) && product_fits(d_out, d_in, m);
 }
 
@@ -613,8 +606,7 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   if (need || db != nullptr) {
     const bool whole = d_out % 8 == 0 && at16(z);
     const int64_t cols = whole ? (l.np + 255) / 256 : (l.np + 63) / 64;
-    const DzArgs a = {dy, dy_f32, z, act, m, d_out, l.np, need && (dx != nullptr || !l.split) ? u16(l.hi) : nullptr,
-                      l.split && dw != nullptr ? u16(l.both) : nullptr, bsum, parts, exps, static_cast<int>(cols),
+    const DzArgs a = {dy, dy_f32, z, act, m, d_out, l.np, need ? u16(l.dz) : nullptr, dw != nullptr ? 1 : 0, bsum, parts, exps, static_cast<int>(cols),
                       static_cast<int>(cols * l.mt)};
     ConvertArgs c = {{x, w_hat}, {u16(l.x16), u16(l.w16)}, {m * d_in / 8, d_out * d_in / 8}, {0, 0}, exps};
     auto blocks = [](int64_t n8) { return static_cast<int>(n8 / 512 + 1 < 2048 ? n8 / 512 + 1 : 2048); };
@@ -632,15 +624,17 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
     hipLaunchKernelGGL(bias_kernel, dim3(static_cast<unsigned>((d_out + 255) / 256)), dim3(256), 0, s, bsum, l.mt, d_out, db);
     if ((rc = w4q_launch_status()) != W4Q_OK) return rc;
   }
-  const uint16_t* hi = l.direct ? static_cast<const uint16_t*>(dy) : u16(l.hi);
+  const uint16_t* dz = l.direct ? static_cast<const uint16_t*>(dy) : u16(l.dz);
+  const int ldz = static_cast<int>(l.split ? 2 * l.np : l.np);
   const bool vec = at16(dx) && at16(dw);  // (rows of d_in, a multiple of 32, values)
   if (dx != nullptr) {  // dx [m][d_in] = dz W: dz along n, W across
     NtArgs g = {};
-    g.a = hi;
+    g.a = dz;
     g.b = l.split ? u16(l.w16) : w_hat;
     g.M = static_cast<int>(m);
     g.N = g.ldb = static_cast<int>(d_in);
-    g.K = g.lda = static_cast<int>(l.np);
+    g.lda = ldz;
+    g.K = static_cast<int>(l.np);
     g.kb = static_cast<int>(d_out);
     const EpiGrad e = {exps, l.split ? exps + 2 : nullptr, dx, 1, vec ? 1 : 0};
     rc = l.split ? lin_product<1, true, false, true>(g, l.px, e, part, s) : lin_product<1, false, false, true>(g, l.px, e, part, s);
@@ -648,11 +642,12 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   }
   if (dw != nullptr) {  // dW [d_out][d_in] = dz^T x: both across
     NtArgs g = {};
-    g.a = l.split ? u16(l.both) : hi;
+    g.a = dz;
     g.b = l.split ? u16(l.x16) : x;
     g.M = static_cast<int>(d_out);
     g.N = g.ldb = static_cast<int>(d_in);
-    g.lda = static_cast<int>(l.split ? 2 * l.np : l.np);
+    g.lda = ldz;
+    g.la = l.split ? static_cast<int>(l.np) : 0;
     g.K = g.ka = g.kb = static_cast<int>(m);
     const EpiGrad e = {exps, l.split ? exps + 1 : nullptr, dw, 0, vec ? 1 : 0};
     rc = l.split ? lin_product<2, true, true, true>(g, l.pw, e, part, s) : lin_product<1, false, true, true>(g, l.pw, e, part, s);
