@@ -500,21 +500,19 @@ BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
 }
 
 // The deployed weights as w4a16_gemm_dq reads them, bf16_RNE(s * q), written out for the product of many
-// rows: a group of 32 codes (16 bytes) per thread, s * (q + 8) - 8 s in one exact fused multiply-add.
-// HBM bound: 2.6 B per weight.
-__global__ __launch_bounds__(256) void dequant_kernel(const u32x4* __restrict__ packed, const uint16_t* __restrict__ s16,
-                                                      int64_t groups, u32x4* __restrict__ w) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= groups) return;
-  const u32x4 c = packed[i];
-  const float s = f16_bits_to_f32(s16[i]), ms = -8.0f * s;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    const uint32_t word = c[d] ^ 0x88888888u;  // codes in offset binary
+// rows: 8 codes per thread (so that a wavefront's stores are consecutive), s * (q + 8) - 8 s in one exact
+// fused multiply-add.  HBM bound: 2.6 B per weight.
+__global__ __launch_bounds__(256) void dequant_kernel(const uint32_t* __restrict__ packed, const uint16_t* __restrict__ s16,
+                                                      int64_t words, u32x4* __restrict__ w) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+#pragma unroll 4
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < words; i += step) {
+    const float s = f16_bits_to_f32(s16[i >> 2]), ms = -8.0f * s;
+    const uint32_t word = packed[i] ^ 0x88888888u;  // codes in offset binary
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(s, static_cast<float>((word >> (4 * e)) & 15u), ms);
-    w[4 * i + d] = pack_bf16(v);
+    w[i] = pack_bf16(v);
   }
 }
 
@@ -574,11 +572,11 @@ size_t w4q_linear_dq_workspace(int64_t m, int64_t d_out, int64_t d_in) {
 int w4q_launch_linear_dq(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16, int64_t d_out,
                          int64_t d_in, const W4Epilogue& ep, void* y, int y_dtype, void* ws, size_t ws_bytes,
                          hipStream_t s) {
-  const int64_t groups = d_out * (d_in / 32);
+  const int64_t words = d_out * (d_in / 8), blocks = (words + 1023) / 1024;
   uint16_t* w = static_cast<uint16_t*>(ws);
   const size_t used = up256(size_t(2) * d_out * d_in);
-  hipLaunchKernelGGL(dequant_kernel, dim3(static_cast<unsigned>((groups + 255) / 256)), dim3(256), 0, s,
-                     reinterpret_cast<const u32x4*>(packed), s16, groups, reinterpret_cast<u32x4*>(w));
+  hipLaunchKernelGGL(dequant_kernel, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s,
+                     reinterpret_cast<const uint32_t*>(packed), s16, words, reinterpret_cast<u32x4*>(w));
   const int rc = w4q_launch_status();
   if (rc != W4Q_OK) return rc;
   return w4q_launch_linear_fwd(x, m, w, d_out, d_in, ep.bias, ep.act, ep.res, nullptr, y, y_dtype,
