@@ -11,6 +11,8 @@ import layer_ref as R
 pytestmark = pytest.mark.gpu
 
 w4q = pytest.importorskip("w4a16_group_wise_amd")
+from w4a16_group_wise_amd._lib import W4QError  # noqa: E402
+
 BF, F32 = torch.bfloat16, torch.float32
 
 
@@ -384,3 +386,45 @@ def test_one_training_step_and_deployment(dev):
             _, yr, _, ey = R.linear_fwd(t, wr, b, a, r)
             ey = ey + R.DACT_MAX * (k + 64) * R.H32 * (t.double().abs() @ wr.abs().t())
             within(got, yr, R.stored(ey, yr, BF), f"deployed {rows}")
+
+
+def test_binding_refuses_overlaps_and_wrong_shapes(dev):
+    m, n, k = 16, 64, 64
+    x, w, scale, bias = layer(m, n, k, dev)
+    packed, s16 = w4q.quant_pack(w, scale)
+    buf = torch.zeros(m * n + 64, dtype=BF, device=dev)
+    y, shifted = buf[:m * n].view(m, n), buf[8:8 + m * n].view(m, n)
+    for call in (lambda **kw: w4q.lsq_linear_fwd(x, w, scale, **kw), lambda **kw: w4q.w4a16_linear(x, packed, s16, out_dtype=BF, **kw)):
+        with pytest.raises(ValueError, match="overlap"):
+            call(residual=shifted, out=y)
+        with pytest.raises(ValueError, match="overlap"):
+            call(out=x)
+        with pytest.raises(ValueError, match="shape"):
+            call(residual=y[:8])
+        with pytest.raises(ValueError, match="shape"):
+            call(bias=bias[:8])
+        with pytest.raises(TypeError):
+            call(residual=y.float())
+        with pytest.raises(ValueError, match="act must be"):
+            call(act="tanh")
+        with pytest.raises(ValueError, match="contiguous"):
+            call(residual=torch.zeros(n, m, dtype=BF, device=dev).t())
+        call(residual=y, out=y)
+    with pytest.raises(ValueError, match="overlap"):
+        w4q.lsq_linear_fwd(x, w, scale, w_hat=w.view(torch.uint8).view(-1)[:2 * n * k].view(BF).view(n, k))
+    with pytest.raises(ValueError, match="together"):
+        w4q.lsq_linear_fwd(x, w, None)
+    with pytest.raises(ValueError, match="needs z"):
+        w4q.lsq_linear_bwd(x, w.to(BF), y, act="silu")
+    with pytest.raises(ValueError, match="no gradient"):
+        w4q.lsq_linear_bwd(x, w.to(BF), y, with_x=False, with_w=False)
+    with pytest.raises(ValueError, match="overlap"):
+        w4q.muon_step(w, w, torch.zeros_like(w), lr=0.1)
+    with pytest.raises(ValueError, match="overlap"):
+        w4q.newton_schulz(w[:32], out=w[16:48])
+    with pytest.raises(W4QError):
+        w4q.newton_schulz(w, steps=0)
+    with pytest.raises(W4QError):
+        w4q.w4a16_linear(x[:0], packed, s16)
+    with pytest.raises(W4QError):
+        w4q.lsq_linear_bwd(x, w.to(BF), y, workspace=torch.empty(16, dtype=torch.uint8, device=dev))

@@ -420,17 +420,21 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_mma_kernel(const uint16_t* _
 // of an item is reduced, its rows are finished (lane reduction, store) and the accumulators
 // restart.  Problems are numbered in the order given; first[p] is the first item of problem p.
 constexpr int kMaxGroup = 64;
-struct GroupArgs {
-  const uint16_t* x[kMaxGroup];
-  const uint8_t* packed[kMaxGroup];
-  const uint16_t* s16[kMaxGroup];
-  void* y[kMaxGroup];
-  int d_out[kMaxGroup];
-  int d_in[kMaxGroup];
-  int first[kMaxGroup + 1];
+template <int N>
+struct GroupArgsOf {
+  const uint16_t* x[N];
+  const uint8_t* packed[N];
+  const uint16_t* s16[N];
+  void* y[N];
+  int d_out[N];
+  int d_in[N];
+  int first[N + 1];
   int n;
   int y_dtype;
 };
+// with an epilogue there is one problem, and a launch does not carry 2.8 KB of arguments
+template <bool kEpi>
+using GroupArgs = GroupArgsOf<kEpi ? 1 : kMaxGroup>;
 
 __device__ __forceinline__ int uniform_int(int v) { return __builtin_amdgcn_readfirstlane(v); }
 template <typename T>
@@ -500,7 +504,7 @@ constexpr int stream_threads() { return kLut ? 512 : 256; }
 // round trip before the first code load: per-phase decode pass of the 36-layer stack 1262 ->
 // 1205 us without it.)
 template <int LPR, int RS, bool kLut, bool kEpi>
-__global__ __launch_bounds__(stream_threads<kLut>()) void gemv_stream_kernel(const GroupArgs t, const W4Epilogue ep) {
+__global__ __launch_bounds__(stream_threads<kLut>()) void gemv_stream_kernel(const GroupArgs<kEpi> t, const W4Epilogue ep) {
   constexpr int kStreamThreads = stream_threads<kLut>();
   __shared__ uint32_t lut[kLut ? 256 * 64 : 1];
   constexpr int RPS = 64 / LPR;
@@ -787,7 +791,7 @@ int resident_grid(const void* kernel, int slot, int threads = kThreads) {
 }
 
 template <int LPR, int RS, bool kLut, bool kEpi>
-int launch_stream(const GroupArgs& a, int64_t items, int slot, hipStream_t s, const W4Epilogue& ep) {
+int launch_stream(const GroupArgs<kEpi>& a, int64_t items, int slot, hipStream_t s, const W4Epilogue& ep) {
   constexpr int nt = stream_threads<kLut>();
   auto* k = &gemv_stream_kernel<LPR, RS, kLut, kEpi>;
   const int res = resident_grid(reinterpret_cast<const void*>(k), slot, nt);
@@ -799,7 +803,7 @@ int launch_stream(const GroupArgs& a, int64_t items, int slot, hipStream_t s, co
 }
 
 template <bool kLut, bool kEpi>
-int launch_stream_lpr(const GroupArgs& a, int64_t items, int lpr, hipStream_t s, const W4Epilogue& ep) {
+int launch_stream_lpr(const GroupArgs<kEpi>& a, int64_t items, int lpr, hipStream_t s, const W4Epilogue& ep) {
   constexpr int base = (kLut ? 0 : 7) + (kEpi ? 14 : 0);  // resident-grid cache slots
   switch (lpr) {
     case 64: return launch_stream<64, 4, kLut, kEpi>(a, items, base + 0, s, ep);
@@ -834,10 +838,10 @@ int64_t chunk_items(const w4q_gemv_problem* probs, int cnt, int lpr) {
 // ones take the byte-select conversion, whose workgroups start streaming at once.  (Measured per
 // launch, 4096x4096 repeated: 5.4 us with the table, 4.0 us without; 24576x4096: 12.3 vs 13.9 us;
 // all 252 linears of the 36-layer stack in 64-problem launches: 699 vs 836 us.)
-// ep: the epilogue of a single problem, or null.
-int launch_group_chunk(const w4q_gemv_problem* probs, int cnt, int y_dtype, hipStream_t s,
-                       const W4Epilogue* ep = nullptr) {
-  GroupArgs a = {};
+// kEpi: a single problem, with the epilogue.
+template <bool kEpi>
+int launch_group_chunk(const w4q_gemv_problem* probs, int cnt, int y_dtype, hipStream_t s, const W4Epilogue& ep) {
+  GroupArgs<kEpi> a = {};
   const int lpr = chunk_lpr(probs, cnt);
   const int rows_per_item = 4 * (64 / lpr);
   int64_t items = 0, bytes = 0;
@@ -857,10 +861,7 @@ int launch_group_chunk(const w4q_gemv_problem* probs, int cnt, int y_dtype, hipS
   a.n = cnt;
   a.y_dtype = y_dtype;
   const bool lut = bytes >= (int64_t(48) << 20) && items >= 4096;
-  if (ep != nullptr)
-    return lut ? launch_stream_lpr<true, true>(a, items, lpr, s, *ep) : launch_stream_lpr<false, true>(a, items, lpr, s, *ep);
-  const W4Epilogue none = {};
-  return lut ? launch_stream_lpr<true, false>(a, items, lpr, s, none) : launch_stream_lpr<false, false>(a, items, lpr, s, none);
+  return lut ? launch_stream_lpr<true, kEpi>(a, items, lpr, s, ep) : launch_stream_lpr<false, kEpi>(a, items, lpr, s, ep);
 }
 
 }  // namespace
@@ -921,7 +922,8 @@ int w4q_launch_gemv(const uint16_t* x, int64_t m, const uint8_t* packed, const u
   }
   const w4q_gemv_problem one = {x, packed, s16, y, d_out, d_in};
   if (d_out <= 0x7FFFFFFF && d_in <= (1 << 24) && w4q_gemv_group_fits(&one, 1))
-    return launch_group_chunk(&one, 1, y_dtype, s, ep);
+    return ep != nullptr ? launch_group_chunk<true>(&one, 1, y_dtype, s, *ep)
+                         : launch_group_chunk<false>(&one, 1, y_dtype, s, W4Epilogue{});
   if (ep != nullptr) return W4Q_EUNSUPPORTED;
   return launch_mt<1>(x, 1, packed, s16, d_out, d_in, y, y_dtype, s);
 }
@@ -942,7 +944,7 @@ bool w4q_gemv_group_fits(const w4q_gemv_problem* probs, int n) {
 // One launch for up to kMaxGroup one-row products (any d_out, d_in % 32 == 0).
 int w4q_launch_gemv_group(const w4q_gemv_problem* probs, int n, int y_dtype, hipStream_t s) {
   for (int b = 0; b < n; b += kMaxGroup) {
-    const int rc = launch_group_chunk(probs + b, n - b < kMaxGroup ? n - b : kMaxGroup, y_dtype, s);
+    const int rc = launch_group_chunk<false>(probs + b, n - b < kMaxGroup ? n - b : kMaxGroup, y_dtype, s, W4Epilogue{});
     if (rc != W4Q_OK) return rc;
   }
   return W4Q_OK;

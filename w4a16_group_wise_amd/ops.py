@@ -443,6 +443,11 @@ def _no_overlap(pairs) -> None:
             raise ValueError(f"{an} and {bn} overlap")
 
 
+def _shifted(residual, y):
+    """The residual, unless it is y itself (which it may be)."""
+    return None if residual is None or residual.data_ptr() == y.data_ptr() else residual
+
+
 def _epilogue(m, d_out, dtype, device, bias, residual) -> None:
     if bias is not None:
         _need(bias, "bias", torch.float32, (d_out,), device)
@@ -470,7 +475,10 @@ def lsq_linear_fwd(x: torch.Tensor, w: Optional[torch.Tensor], scale: Optional[t
             raise ValueError(f"w must be [d_out][{d_in}], got {tuple(w.shape)}")
         d_out = w.shape[0]
         _need(scale, "scale", torch.float32, (d_out, d_in // W4Q_GROUP), x.device)
-        w_hat = _out(w_hat, "w_hat", (d_out, d_in), torch.bfloat16, x.device)
+        if w_hat is not None:
+            _need(w_hat, "w_hat", torch.bfloat16, (d_out, d_in), x.device)
+            _no_overlap((((w_hat, "w_hat"), (t, n)) for t, n in ((x, "x"), (w, "w"), (scale, "scale"), (bias, "bias"),
+                                                                 (residual, "residual"))))
     else:
         if w_hat is None:
             raise ValueError("w and scale, or w_hat, must be given")
@@ -480,10 +488,13 @@ def lsq_linear_fwd(x: torch.Tensor, w: Optional[torch.Tensor], scale: Optional[t
         d_out = w_hat.shape[0]
     _epilogue(m, d_out, out_dtype, x.device, bias, residual)
     with _OnDevice(x.device):
+        if w_hat is None:
+            w_hat = torch.empty((d_out, d_in), dtype=torch.bfloat16, device=x.device)
         y = _out(out, "y", (m, d_out), out_dtype, x.device)
         z = torch.empty((m, d_out), dtype=torch.bfloat16, device=x.device) if with_z else None
         if out is not None:
-            _no_overlap((((y, "out"), (t, n)) for t, n in ((x, "x"), (w, "w"), (w_hat, "w_hat"))))
+            _no_overlap((((y, "out"), (t, n)) for t, n in ((x, "x"), (w, "w"), (scale, "scale"), (w_hat, "w_hat"),
+                                                           (bias, "bias"), (_shifted(residual, y), "residual"))))
         wp, wb, _keep = _scratch("lsq_linear_fwd_workspace_size", (m, d_out, d_in), x.device, workspace)
         check("lsq_linear_fwd", lib().lsq_linear_fwd(
             x.data_ptr(), m, _ptr(w), _ptr(scale), d_out, d_in, _ptr(bias), a, _ptr(residual), w_hat.data_ptr(),
@@ -542,7 +553,8 @@ def w4a16_linear(x: torch.Tensor, packed: torch.Tensor, scale_f16: torch.Tensor,
     with _OnDevice(x.device):
         y = _out(out, "y", (m, d_out), out_dtype, x.device)
         if out is not None:
-            _no_overlap((((y, "out"), (t, n)) for t, n in ((x, "x"), (packed, "packed"), (scale_f16, "scale_f16"))))
+            _no_overlap((((y, "out"), (t, n)) for t, n in ((x, "x"), (packed, "packed"), (scale_f16, "scale_f16"),
+                                                           (bias, "bias"), (_shifted(residual, y), "residual"))))
         wp, wb, _keep = _scratch("w4a16_linear_workspace_size", (m, d_out, d_in, 1 if dequant_bf16 else 0), x.device,
                                  workspace)
         check("w4a16_linear", lib().w4a16_linear(
