@@ -9,8 +9,9 @@
  *
  * The conventions of w4a16q.h hold (device memory, row-major and contiguous, work enqueued on
  * `stream`, nothing allocated or synchronised, argument errors reported before anything is
- * enqueued, every call can be captured in a HIP graph).  Calls that may overlap need distinct
- * workspaces.  All results are run-to-run deterministic.
+ * enqueued, every call can be captured in a HIP graph).  Outputs must not overlap inputs or each
+ * other except where named.  Calls that may overlap in time need distinct workspaces.  All results
+ * are run-to-run deterministic.
  */
 #ifndef W4A16Q_LAYER_H
 #define W4A16Q_LAYER_H
