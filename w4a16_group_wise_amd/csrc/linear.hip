@@ -423,8 +423,8 @@ __global__ __launch_bounds__(256) void dz_ragged_kernel(const DzArgs a, const Co
 }
 
 // dbias: the tiles' column sums added in fp64 (one rounding at the end), in a fixed order: 32 columns x 8
-// runs of tiles to a workgroup, each thread its run in row order, then the runs (latency bound: 262144 x 256 rows and columns
-// with the pass over dz: 179 us with one thread per column, 39 us here)
+// runs of tiles to a workgroup, each thread its run in row order, then the runs (latency bound: 262144 x 256
+// with the pass over dz: 179 us with one thread per column, 39 us so)
 __global__ __launch_bounds__(256) void bias_kernel(const float* __restrict__ bsum, int64_t tiles, int64_t n,
                                                    float* __restrict__ db) {
   __shared__ double runs[8][32];
@@ -449,13 +449,13 @@ template <int PA, bool F16, bool AT, bool BT>
 using Big = NtCfg<256, 256, 128, 64, PA, 1, F16, AT, BT>;
 template <int PA, bool F16, bool AT, bool BT>
 using Mid = NtCfg<128, 128, 64, 64, PA, 1, F16, AT, BT>;
-// where no compute unit gets two workgroups, eight wavefronts a tile rather than four: two on each SIMD
+// where no compute unit gets two workgroups, eight wavefronts a tile rather than four, two on each SIMD
 // (1531x2050x1056 forward: 38.5 -> 34.3 us; with two workgroups on a compute unit four are better,
-// 2048x4096x4096: 95 and 105 us)
+// 2048x4096x4096: 95 and 105 us), and a third stage buffer (2048x2048x4096 forward 49 -> 45.5 us)
 template <int PA, bool F16, bool AT, bool BT>
-using MidAlone = NtCfg<128, 128, 64, 32, PA, 1, F16, AT, BT>;
+using MidAlone = NtCfg<128, 128, 64, 32, PA, 1, F16, AT, BT, false, 3>;
 template <int PA, bool F16, bool AT, bool BT>
-using Small = NtCfg<64, 64, 32, 32, PA, 1, F16, AT, BT>;
+using Small = NtCfg<64, 64, 32, 32, PA, 1, F16, AT, BT, false, 3>;
 
 // parts: of the first operand; tiny: whether the small-product kernel takes the form (both along k)
 NtPlan lin_plan(int64_t M, int64_t N, int64_t K, int parts, bool tiny, bool split = true) {

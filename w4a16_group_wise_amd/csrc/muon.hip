@@ -325,10 +325,12 @@ template <bool AT, bool BT>
 using Big = NtCfg<256, 256, 128, 64, 2, 2, true, AT, BT>;
 template <bool AT, bool BT>
 using Mid = NtCfg<128, 128, 64, 64, 2, 2, true, AT, BT>;
+// no compute unit with two workgroups: eight wavefronts a tile (two on each SIMD) and a third stage buffer
+// (2048x2048, five steps: 783 -> 772 and 765 -> 749 us)
 template <bool AT, bool BT>
-using MidAlone = NtCfg<128, 128, 64, 32, 2, 2, true, AT, BT>;
+using MidAlone = NtCfg<128, 128, 64, 32, 2, 2, true, AT, BT, false, 3>;
 template <bool AT, bool BT>
-using Small = NtCfg<64, 64, 32, 32, 2, 2, true, AT, BT, true>;
+using Small = NtCfg<64, 64, 32, 32, 2, 2, true, AT, BT, true, 3>;
 
 NtPlan ns_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri) {
   return nt_plan(batch, M, N, K, tri, 32, 2.4, true, true);

@@ -21,10 +21,13 @@
 // as their producers wrote them.
 //
 // Mapping: BM x BN output tiles, wavefronts of WM x WN (32x32 blocks of v_mfma_f32_32x32x16).
-// Two stage buffers and one barrier per stage, before the stage's last step of 16 k: there every
-// wavefront holds the last fragments of the stage in registers and the next stage has landed, so after
-// it the loads of the stage after next go into the buffer just read (they have a whole stage to
-// land) and the first fragments of the next stage are read between the products of the last step.
+// Two stage buffers, or three, and one barrier per stage, before the stage's last step of 16 k: there
+// every wavefront holds the last fragments of the stage in registers and the next stage has landed, so
+// after it the loads of the stage after next (of three: the one behind it) go into the buffer just read
+// and the first fragments of the next stage are read between the products of the last step.  With two
+// they have one stage to land, which on 64x64 tiles is too short: a third buffer took 0.155 to 0.12 units a
+// stage there (1024x1024, five steps of 2 x 2 parts: 284 -> 200 us with the plan that follows from it); a
+// fourth gained nothing, nor did a third on 128x128 tiles with two workgroups on a compute unit.
 // Rows and k past an operand's end read as zeros (the buffer's bounds); columns past the end of an
 // "across" row read on into the next row and only feed outputs that are never stored.
 //
@@ -179,7 +182,7 @@ struct NtOperand {
   }
 };
 
-template <int BM_, int BN_, int WM_, int WN_, int PA_, int PB_, bool F16_, bool AT_, bool BT_, bool LOLO_ = false>
+template <int BM_, int BN_, int WM_, int WN_, int PA_, int PB_, bool F16_, bool AT_, bool BT_, bool LOLO_ = false, int BUFS_ = 2>
 struct NtCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PA = PA_, PB = PB_;
   static constexpr bool F16 = F16_, AT = AT_, BT = BT_, LOLO = LOLO_;  // AT, BT: operand lies across
@@ -191,7 +194,8 @@ struct NtCfg {
   using OpB = NtOperand<BN, PB, BT, BK, kWaves>;
   static constexpr int kOps = OpA::kLoads + OpB::kLoads;              // loads per wave and stage
   static constexpr int kStage = OpA::kBytes + OpB::kBytes;
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kBufs = BUFS_;                                 // stage buffers
+  static constexpr int kLds = kBufs * kStage;
   static constexpr int kTileElems = BM * BN;
   static constexpr int kPitch = WN + 4;                               // floats per row of an epilogue strip
   static constexpr int kReads = PA * MB * (AT ? 2 : 1) + PB * NB * (BT ? 2 : 1);  // LDS reads per step
@@ -421,9 +425,9 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
       __builtin_amdgcn_sched_barrier(0);
     };
     Frags f0, f1;
-    issue(s0, 0);
-    issue(s0 + 1, 1);
-    sync(std::integral_constant<int, C::kOps>{});  // stage s0 has landed
+#pragma unroll
+    for (int i = 0; i < C::kBufs; ++i) issue(s0 + i, i);
+    sync(std::integral_constant<int, C::kOps * (C::kBufs - 1)>{});  // stage s0 has landed
     load(0, 0, f0);
     int buf = 0;
     for (int s = s0; s < s1; ++s) {
@@ -433,9 +437,10 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
         mma((kk & 1) != 0 ? f1 : f0);
         pattern();
       }
-      sync(std::integral_constant<int, 0>{});  // stage s + 1 has landed; nobody reads buffer `buf` any more
-      issue(s + 2, buf);
-      buf ^= 1;
+      // stage s + 1 has landed; nobody reads buffer `buf` any more
+      sync(std::integral_constant<int, C::kOps * (C::kBufs - 2)>{});
+      issue(s + C::kBufs, buf);
+      buf = buf + 1 == C::kBufs ? 0 : buf + 1;
       load(buf, 0, f0);  // (past the range: a buffer of zeros, never used)
       mma(f1);
       pattern();
@@ -634,7 +639,7 @@ struct NtTile {
   int edge, per_cu;
   double busy, alone;
 };
-constexpr NtTile kNtTiles[4] = {{256, 1, 1.0, 0.70}, {128, 2, 0.265, 0.35}, {64, 4, 0.098, 0.155}, {32, 1, 0.0, 0.0}};
+constexpr NtTile kNtTiles[4] = {{256, 1, 1.0, 0.70}, {128, 2, 0.265, 0.35}, {64, 3, 0.098, 0.120}, {32, 1, 0.0, 0.0}};
 
 inline NtPlan nt_plan_tile(int kind, int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, int BK) {
   NtPlan p;
@@ -655,7 +660,7 @@ inline NtPlan nt_plan_tile(int kind, int64_t batch, int64_t M, int64_t N, int64_
 // partial tiles then pass through memory once more (5 us and 3 TB/s measured).  Sizes with the same
 // estimate take the larger tile.  E.g. 2 x 2 parts at 2048 cubed: 112 us on 64 tiles of 256, 52 us on
 // 256 of 128, 59 us on 1024 of 64; 1024 cubed: 56, 22, 12 us; 512 x 512 x 8192: 398, 143, 106 us
-// whole and 42, 29, 30 us in ranges.
+// whole and 42, 29, 30 us in ranges (all with two stage buffers).
 inline NtPlan nt_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, int BK, double unit_us, bool split,
                       bool tiny) {
   NtPlan best = {};
