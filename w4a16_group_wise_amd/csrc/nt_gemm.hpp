@@ -74,7 +74,8 @@ struct NtArgs {
   int tri;            // 1: M == N and only tiles with row tile >= column tile
   int per_batch;      // tiles of one batch
   int S;              // stages per tile
-  int total;          // iterations (batches * per_batch * S)
+  int whole;          // tiles a workgroup takes whole: tiles lb, lb + nblk, ...
+  int rest;           // iterations of the tiles behind those, cut into ranges of `chunk`
   int chunk, nblk, per_xcd;
   float* ws;
 };
@@ -328,8 +329,9 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
   const int lb = static_cast<int>(blockIdx.x & 7) * g.per_xcd + static_cast<int>(blockIdx.x >> 3);
   if (lb >= g.nblk) return;
-  const int it_begin = lb * g.chunk;
-  const int it_end = g.total - it_begin < g.chunk ? g.total : it_begin + g.chunk;
+  const int whole_end = g.whole * g.S;  // iterations of the whole tiles, then of the range
+  const int left = g.rest - lb * g.chunk;
+  const int end = whole_end + (left < 0 ? 0 : left < g.chunk ? left : g.chunk);
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -347,11 +349,20 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
 #pragma unroll
   for (int j = 0; j < C::NB; ++j) bro[j] = OpB::read_off(wn * C::WN + 32 * j, lane);
 
-  int it = it_begin;
-  while (it < it_end) {
-    const int t = it / g.S;
-    const int s0 = it - t * g.S;
-    const int s1 = g.S - s0 < it_end - it ? g.S : s0 + (it_end - it);
+  int it = 0;
+  while (it < end) {
+    int t, s0, s1;
+    if (it < whole_end) {
+      t = it / g.S * g.nblk + lb;
+      s0 = 0;
+      s1 = g.S;
+    } else {
+      const int at = lb * g.chunk + (it - whole_end);
+      t = at / g.S;
+      s0 = at - t * g.S;
+      s1 = g.S - s0 < end - it ? g.S : s0 + (end - it);
+      t += g.whole * g.nblk;
+    }
     int batch, ti, tj;
     nt_tile(g, t, batch, ti, tj);
     const int m0 = ti * C::BM, n0 = tj * C::BN;
@@ -461,9 +472,9 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
         nt_strip_store<C>(g, epi, batch, row0 + 32 * i, col0, ti == tj, lane, strip, pre[i % kSets]);
         if (Epi::kLoads == 1 && i + 1 < C::MB) nt_strip_load<C>(g, epi, batch, row0 + 32 * (i + 1), col0, lane, pre[0]);
       }
-      if (it + (s1 - s0) < it_end) sync(std::integral_constant<int, 0>{});  // the next tile's loads reuse the LDS
+      if (it + (s1 - s0) < end) sync(std::integral_constant<int, 0>{});  // the next tile's loads reuse the LDS
     } else {
-      float* slot = g.ws + static_cast<int64_t>(2 * lb + (it == it_begin ? 0 : 1)) * C::kTileElems;
+      float* slot = g.ws + static_cast<int64_t>(2 * lb + (it == whole_end ? 0 : 1)) * C::kTileElems;
 #pragma unroll
       for (int i = 0; i < C::MB; ++i)
 #pragma unroll
@@ -485,7 +496,7 @@ template <class C, class Epi>
 __global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi epi) {
   __shared__ __attribute__((aligned(16))) float strip[32 * C::kPitch];
   constexpr int kStrips = C::kWaves * C::MB;  // strips of a tile
-  const int t = static_cast<int>(blockIdx.x) / kStrips;
+  int t = static_cast<int>(blockIdx.x) / kStrips;
   const int64_t b0 = static_cast<int64_t>(t) * g.S;
   const int first = static_cast<int>(b0 / g.chunk);
   const int last = static_cast<int>((b0 + g.S - 1) / g.chunk);
@@ -493,6 +504,7 @@ __global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi 
   const int lane = threadIdx.x & 63;
   const int si = static_cast<int>(blockIdx.x) % kStrips;
   const int wid = si / C::MB, i = si % C::MB;
+  t += g.whole * g.nblk;
   int batch, ti, tj;
   nt_tile(g, t, batch, ti, tj);
   const int row0 = ti * C::BM + (wid / C::kWavesN) * C::WM + 32 * i;
@@ -628,7 +640,7 @@ constexpr int kNtMinK = 512;  // k a range covers at least
 
 struct NtPlan {
   int kind;  // tile: 0 256x256, 1 128x128, 2 64x64, 3 32x32 (small products)
-  int64_t tm, tn, per_batch, S, total, chunk, nblk;
+  int64_t tm, tn, per_batch, S, total, whole, rest, chunk, nblk;
   size_t ws;  // scratch bytes (0: no tile is split)
 };
 
@@ -650,7 +662,8 @@ inline NtPlan nt_plan_tile(int kind, int64_t batch, int64_t M, int64_t N, int64_
   p.per_batch = tri ? p.tm * (p.tm + 1) / 2 : p.tm * p.tn;
   p.S = (K + BK - 1) / BK;
   p.total = batch * p.per_batch * p.S;
-  p.chunk = p.S;
+  p.whole = 1;
+  p.rest = p.chunk = 0;
   p.nblk = batch * p.per_batch;
   p.ws = 0;
   return p;
@@ -677,16 +690,20 @@ inline NtPlan nt_plan(int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, 
       best_us = us;
     }
     if (!split) continue;
+    // as many whole tiles as every resident workgroup gets, the rest in ranges
     const int64_t slots = kNtCus * t.per_cu;
-    int64_t chunk = (p.total + slots - 1) / slots;
-    if (chunk < kNtMinK / BK) chunk = kNtMinK / BK;
-    if (chunk % p.S == 0) continue;
-    p.chunk = chunk;
-    p.nblk = (p.total + chunk - 1) / chunk;
-    p.ws = static_cast<size_t>(p.nblk) * 2 * t.edge * t.edge * sizeof(float);
-    const double load = static_cast<double>(p.total) * t.busy / kNtCus;  // evenly spread
-    const double alone = static_cast<double>(chunk) * t.alone;
-    const double bytes = static_cast<double>(p.nblk + tiles) * t.edge * t.edge * 4.0;
+    p.whole = tiles / slots;
+    p.rest = (tiles - p.whole * slots) * p.S;
+    if (p.rest == 0) continue;
+    p.chunk = (p.rest + slots - 1) / slots;
+    if (p.chunk < kNtMinK / BK) p.chunk = kNtMinK / BK;
+    const int64_t ranges = (p.rest + p.chunk - 1) / p.chunk;
+    if (p.chunk % p.S == 0) continue;
+    p.nblk = p.whole != 0 ? slots : ranges;
+    p.ws = static_cast<size_t>(ranges) * 2 * t.edge * t.edge * sizeof(float);
+    const double load = (static_cast<double>(p.whole) * t.per_cu * p.S + static_cast<double>(p.rest) / kNtCus) * t.busy;
+    const double alone = static_cast<double>(p.chunk) * t.alone + static_cast<double>(p.whole) * t.per_cu * p.S * t.busy;
+    const double bytes = static_cast<double>(ranges + p.rest / p.S) * t.edge * t.edge * 4.0;
     const double sus = 9.0 + unit_us * (load > alone ? load : alone) + bytes / 3e6;
     if (sus < best_us) {
       best = p;
@@ -713,7 +730,8 @@ inline void nt_fill(NtArgs& g, const NtPlan& p, int tri, void* ws) {
   g.tri = tri;
   g.per_batch = static_cast<int>(p.per_batch);
   g.S = static_cast<int>(p.S);
-  g.total = static_cast<int>(p.total);
+  g.whole = static_cast<int>(p.whole);
+  g.rest = static_cast<int>(p.rest);
   g.chunk = static_cast<int>(p.chunk);
   g.nblk = static_cast<int>(p.nblk);
   g.per_xcd = (g.nblk + 7) / 8;
@@ -736,8 +754,7 @@ int nt_launch(NtArgs g, const NtPlan& p, int tri, const Epi& epi, void* ws, hipS
   int rc = w4q_launch_status();
   if (rc == W4Q_OK && p.ws != 0) {
     constexpr int per_tile = C::kWaves * C::MB;
-    const int64_t tiles = p.total / p.S;
-    hipLaunchKernelGGL((nt_fixup_kernel<C, Epi>), dim3(static_cast<unsigned>(tiles * per_tile)), dim3(64), 0, s, g, epi);
+    hipLaunchKernelGGL((nt_fixup_kernel<C, Epi>), dim3(static_cast<unsigned>(p.rest / p.S * per_tile)), dim3(64), 0, s, g, epi);
     rc = w4q_launch_status();
   }
   return rc;
