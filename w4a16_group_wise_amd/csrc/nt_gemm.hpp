@@ -35,10 +35,12 @@
 // LDS and hands the functor 8 consecutive columns of a row per lane, so that everything the epilogue
 // reads and writes moves in 16-byte pieces; what it reads is loaded ahead.
 //
-// Work split: the (tile, stage) iterations of all tiles lie on one line, cut into nblk equal
-// ranges, one per workgroup.  A range that covers a whole tile ends in the epilogue; partial tiles
-// go to fp32 scratch and are summed by nt_fixup_kernel in k order (a fixed order: results do not
-// depend on timing).  With chunk = stages per tile this is one tile per workgroup and no scratch.
+// Work split: one tile per workgroup; or as many whole tiles as each of the workgroups that fit the
+// device gets, and the (tile, stage) iterations of the remaining tiles on one line, cut into equal ranges,
+// one per workgroup.  Partial tiles go to fp32 scratch and are summed by nt_fixup_kernel in k order (a
+// fixed order: results do not depend on timing).  Ranges start at different k, so their workgroups do not
+// share panels in the L2: with all 528 tiles of a symmetric 4096 cubed product in ranges it took 265 us, with 512
+// of them whole and 16 in ranges about 190.
 #pragma once
 
 #include <type_traits>
@@ -669,8 +671,8 @@ inline NtPlan nt_plan_tile(int kind, int64_t batch, int64_t M, int64_t N, int64_
   return p;
 }
 
-// The cheapest of: whole tiles of each size, and (split) equal ranges of stages of each size, whose
-// partial tiles then pass through memory once more (5 us and 3 TB/s measured).  Sizes with the same
+// The cheapest of: one tile of each size per workgroup, and (split) whole tiles with the remaining ones in
+// ranges, whose partial tiles then pass through memory once more (5 us and 3 TB/s measured).  Sizes with the same
 // estimate take the larger tile.  E.g. 2 x 2 parts at 2048 cubed: 112 us on 64 tiles of 256, 52 us on
 // 256 of 128, 59 us on 1024 of 64; 1024 cubed: 56, 22, 12 us; 512 x 512 x 8192: 398, 143, 106 us
 // whole and 42, 29, 30 us in ranges (all with two stage buffers).
