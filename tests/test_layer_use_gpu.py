@@ -54,7 +54,7 @@ def test_large_forward_and_backward(dev, m, n, k, act):
     within(gb, db, R.stored(eb, db, F32), "grad_bias")
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 4096, 12288), (2, 12288, 512), (16, 9000, 256), (11, 1024, 8192), (700, 2050, 1024),
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 12288), (2, 12288, 512), (16, 9000, 256), (11, 1024, 8192), (40, 12288, 1536), (65, 12288, 1536), (700, 2050, 1024),
                                    (1600, 4096, 4096), (1537, 8200, 2304)])
 @pytest.mark.parametrize("dq", [False, True])
 def test_large_deployed_layer(dev, m, n, k, dq):

@@ -19,8 +19,8 @@ __device__ __forceinline__ float sigmoid(float z) {
 
 // The normal distribution function Phi(z), and exp(-z^2 / 2) beside it, by Abramowitz and Stegun's
 // 7.1.26: for x = |z| / sqrt(2), erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2) + e, t = 1 / (1 + p x),
-// |e| <= 1.5e-7 exp(-x^2)-fold small in the tail, so Phi is within 7.5e-8 (a few 2^-24) absolutely and
-// keeps its leading digits for large negative z.  About 16 instructions; the library's erfc took 40 us
+// |e| <= 1.5e-7, falling with exp(-x^2): Phi is within 7.5e-8 (a few 2^-24) absolutely and keeps its
+// leading digits for large negative z.  About 16 instructions; the library's erfc took 40 us
 // of a 1531 x 2050 gelu epilogue.
 __device__ __forceinline__ float normal_cdf(float z, float& gauss) {
   const float x = __builtin_fabsf(z) * 0.70710678118654752f;

@@ -571,10 +571,11 @@ int w4q_launch_linear_fwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
 
 // Rows from which w4a16_linear writes the dequantised weights out and runs the layer product on them,
 // rather than dequantising in the product's registers (gemm.hip): any number up to 2^24 weights, 1536 on
-// larger ones, where the write costs as much as it saves before (and the scratch is large).  Measured (in
+// larger ones, where the write costs what it saves before (and the scratch is large).  Measured (in
 // registers / written out): 2048x2048 24 rows 43 / 18 us, 2048 rows 107 / 35; 4096x4096 24 rows 51 / 25, 256
-// rows 49 / 35, 2048 rows 153 / 81; 12288x4096 256 rows 62 / 66, 768 rows 123 / 129, 2048 rows 375 / 245;
-// 4096x12288 256 rows 59 / 70, 768 rows 113 / 152, 2048 rows 270 / 230.
+// rows 49 / 35, 2048 rows 153 / 81; 12288x4096 17 rows 56 / 49, 64 rows 62 / 58, 256 rows 62 / 66, 768 rows
+// 123 / 129, 2048 rows 375 / 245; 4096x12288 17 rows 54 / 51, 256 rows 59 / 70, 2048 rows 270 / 230; 20480x4096
+// 17 rows 69 / 74.
 constexpr int64_t kDqRows = 1536, kDqWeights = int64_t(1) << 24;
 size_t w4q_linear_dq_workspace(int64_t m, int64_t d_out, int64_t d_in) {
   if ((m < kDqRows && d_out * d_in > kDqWeights) || d_in % 256 != 0 || !fits(m, d_out, d_in)) return 0;
