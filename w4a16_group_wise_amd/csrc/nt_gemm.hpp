@@ -581,6 +581,10 @@ __global__ __launch_bounds__(C::kThreads) void nt_tiny_kernel(const NtArgs g, co
     OpA::issue(abase, s, s < g.S, m0, C::AT ? g.ka : g.M, g.lda, g.la, g.K, dst, 0, lane, avo);
     OpB::issue(bbase, s, s < g.S, n0, C::BT ? g.kb : g.N, g.ldb, g.lb, g.K, dst + OpA::kBytes, 0, lane, bvo);
   };
+  // the first wavefront does the epilogue: what that reads is on its way before the operands
+  typename Epi::Pre pre[NtStrip<C>::kPasses];
+  if (wid == 0 && Epi::kLoads != 0) nt_strip_load<C>(g, epi, batch, m0, n0, lane, pre);
+  asm volatile("" ::: "memory");
   f32x16 acc[1];
 #pragma unroll
   for (int r = 0; r < 16; ++r) acc[0][r] = 0.0f;
@@ -630,8 +634,6 @@ __global__ __launch_bounds__(C::kThreads) void nt_tiny_kernel(const NtArgs g, co
     for (int w = 1; w < C::kWaves; ++w) v += strip[w * kStride + at];
     strip[at] = v;
   }
-  typename Epi::Pre pre[NtStrip<C>::kPasses];
-  if (wid == 0 && Epi::kLoads != 0) nt_strip_load<C>(g, epi, batch, m0, n0, lane, pre);
   __syncthreads();
   if (wid == 0) nt_strip_store<C>(g, epi, batch, m0, n0, ti == tj, lane, strip, pre);
 }
