@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kThreads) void lsq_fwd_kernel(const float* __restri
 }
 
 // The same forward with the result in the 16-bit activation format, bf16_RNE(fl32(D * code(w, D))),
-// for the layer's product (linear.hip): 6 B per weight + 4 per group, HBM bound.
+// for the layer's product (linear.hip): 6 B per weight + 4 per group, HBM bound (12288x4096: 66 us).
 __global__ __launch_bounds__(kThreads) void lsq_fwd16_kernel(const float* __restrict__ w,
                                                              const float* __restrict__ scale, int64_t n8,
                                                              uint16_t* __restrict__ w_hat) {
