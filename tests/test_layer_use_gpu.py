@@ -155,6 +155,47 @@ def test_special_values_stay_in_their_matrix_row_or_column(dev):
             assert torch.equal(gx[:, cols], gx0[:, cols]) and bool(torch.isnan(gx[:, 5]).all())
 
 
+def test_offsets_past_32_bits(dev):
+    # 2^32 outputs and more: the first and the last rows, and the last matrix of a batch
+    m, n, k = 1 << 20, 4096 + 32, 32
+    x, w, scale, bias = layer(8, n, k, dev, seed=2)
+    x = x.repeat(m // 8, 1)
+    ends = torch.cat((torch.arange(100, device=dev), torch.arange(m - 100, m, device=dev)))
+    x[ends] = torch.randn(200, k, generator=R.gen(1, dev), device=dev).to(BF)
+    y, w_hat, z = w4q.lsq_linear_fwd(x, w, scale, bias=bias, act="silu", with_z=True)
+    zr, yr, ez, ey = R.linear_fwd(x[ends], w_hat, bias, "silu", None)
+    within(y[ends], yr, R.stored(ey, yr, BF), "y")
+    within(z[ends], zr, R.stored(ez, zr, BF), "z")
+    packed, s16 = w4q.quant_pack(w, scale)
+    res = y[ends]
+    out = w4q.w4a16_linear(x, packed, s16, bias=bias, act="silu", residual=y, out_dtype=BF, out=y)
+    wr = R.codes(w, scale) * s16.double().repeat_interleave(32, dim=1)
+    _, yr, _, ey = R.linear_fwd(x[ends], wr, bias, "silu", res)
+    ey = ey + R.DACT_MAX * (k + 64) * R.H32 * (x[ends].double().abs() @ wr.abs().t())
+    within(out[ends], yr, R.stored(ey, yr, BF), "deployed")
+    del out
+    # gradients whose other rows are zero are those of the ends alone
+    gy = y.zero_()
+    gy[ends] = torch.randn(200, n, generator=R.gen(3, dev), device=dev).to(BF)
+    gx, gw, gb = w4q.lsq_linear_bwd(x, w_hat, gy, act="silu", z=z, with_bias=True)
+    _, dx, dw, db, ex, ew, eb = R.linear_bwd(x[ends], w_hat, gy[ends], z[ends], "silu")
+    within(gx[ends], dx, R.stored(ex, dx, BF), "grad_x")
+    within(gw, dw, R.stored(ew, dw, F32), "grad_w_hat")
+    within(gb, db, R.stored(eb, db, F32), "grad_bias")
+    assert bool((gx[100:m - 100] == 0).all())
+    del x, y, z, gy, gx
+    b, r, c = 600, 1500, 5000
+    g = torch.zeros(b, r, c, device=dev)
+    g[0], g[b - 1] = (R.gradient(R.gen(i, dev), r, c, device=dev) for i in (1, 2))
+    o = w4q.newton_schulz(g, out=g)
+    for i, seed in ((0, 1), (b - 1, 2)):
+        ref, err = R.newton_schulz(R.gradient(R.gen(seed, dev), r, c, device=dev))
+        assert float(torch.linalg.vector_norm(o[i].double() - ref)) <= float(err)
+    assert bool((o[1:b - 1] == 0).all())
+    del g, o
+    torch.cuda.empty_cache()
+
+
 # --------------------------------------------------------------------------------- addresses
 def test_element_aligned_views(dev):
     # what the interface lets begin at any element gives the bits of the aligned call
