@@ -660,7 +660,7 @@ struct NtTile {
   int edge, per_cu;
   double busy, alone;
 };
-constexpr NtTile kNtTiles[4] = {{256, 1, 1.0, 0.70}, {128, 2, 0.265, 0.35}, {64, 3, 0.098, 0.120}, {32, 1, 0.0, 0.0}};
+constexpr NtTile kNtTiles[4] = {{256, 1, 1.0, 0.70}, {128, 2, 0.265, 0.31}, {64, 3, 0.098, 0.120}, {32, 1, 0.0, 0.0}};
 
 inline NtPlan nt_plan_tile(int kind, int64_t batch, int64_t M, int64_t N, int64_t K, bool tri, int BK) {
   NtPlan p;
