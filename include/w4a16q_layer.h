@@ -66,7 +66,7 @@ int lsq_linear_fwd_workspace_size(int64_t m, int64_t d_out, int64_t d_in, size_t
  *   grad_y     [m][d_out] fp32 (grad_y_dtype 0) or bf16 (1), 16-B aligned.
  *   z          bf16 [m][d_out]; NULL only with W4Q_ACT_NONE.
  *   grad_x, grad_w_hat, grad_bias   outputs; each may be NULL, not all three.
- *   dz enters grad_w_hat in 22 bits and grad_x in 11 (with W4Q_ACT_NONE and bf16 grad_y: as it
+ *   dz enters both products in 22 bits (with bf16 grad_y and W4Q_ACT_NONE or W4Q_ACT_RELU: as it
  *   is), relative to values within 2^-24 of the largest |grad_y|.
  *   workspace  lsq_linear_bwd_workspace_size bytes, 256-B aligned (W4Q_EINVAL if smaller or NULL).
  *   Limits: as for the forward, with m <= 4194240, d_out <= 2^20 and at most 2^24 - 2^13 blocks of

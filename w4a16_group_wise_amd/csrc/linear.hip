@@ -14,13 +14,15 @@
 //
 // Backward: the products read their operands across their rows where they lie so (dx: W; dW: dz and
 // x), so nothing is transposed in memory.  dW and dbias are fp32 results, so dz may not be rounded
-// to bf16: with an activation (or fp32 dy) dz is held as two fp16 parts, 22 bits, and dW = lo x +
+// to bf16: with gelu and silu (or fp32 dy) dz is held as two fp16 parts, 22 bits, and dW = lo x +
 // hi x.  A bf16 value has 8 bits, so x and W are exact in fp16 once a power of two brings their
 // largest value to 2^14 (values below 2^-32 of the largest lose bits, an absolute error of 2^-40 of
 // it); the exponents come from one maximum over each tensor and are taken back in the epilogue.
-// dx is a bf16 result and takes the hi part alone (11 bits, an eighth of the output's own rounding).
-// Without an activation dz = dy is bf16 already: one exact bf16 product each, no scaling, and x, W
-// and (unless its rows need padding) dy are read as they are.
+// dx takes both parts too: with the hi part alone (11 bits) one result in 25 was another bf16 value
+// than the sum's own rounding; the second product costs a quarter of the call (8192x12288x4096 2199 ->
+// 2710 us).
+// Without an activation and with relu dz (dy, or 0) is bf16 already: one exact bf16 product each, no scaling,
+// and x, W and (without an activation, unless its rows need padding) dy are read as they are.
 #include "epilogue.hpp"
 #include "nt_gemm.hpp"
 
@@ -243,8 +245,9 @@ __device__ __forceinline__ void convert_part(const ConvertArgs& a, int t, int bl
   for (int64_t i = first + step; i < a.n8[t]; i += step) put(i, reinterpret_cast<const u32x4*>(a.src[t])[i]);
 }
 
-// dz = dy act'(z), rows padded to np values with zeros: as two fp16 parts of dz 2^e (kSplit), or (no
-// activation, bf16 dy) dy itself; and column sums over the workgroup's 64 rows for dbias.  A thread has
+// dz = dy act'(z), rows padded to np values with zeros: as two fp16 parts of dz 2^e (kSplit; the parts of
+// 32 columns side by side, as nt_gemm.hpp takes them along and across), or as bf16 (bf16 dy and no
+// activation or relu: exact); and column sums over the workgroup's 64 rows for dbias.  A thread has
 // 8 columns of a row, a workgroup 256 columns x 64 rows, 8 rows at a time.  HBM bound: dy and z read,
 // 4 (2) B written per value (8192x12288x4096
 // with the conversions: 1.14 GB in 198 us).
@@ -255,8 +258,7 @@ struct DzArgs {
   const uint16_t* z;
   int act;
   int64_t m, n, np;
-  uint16_t* out;      // [m][np], or with two parts [m][hi np, lo np]; null (not with parts): not wanted
-  int lo;             // the second part is wanted
+  uint16_t* out;      // [m][np], or with two parts [m][np / 32][hi 32, lo 32]; null (not with parts): not wanted
   float* bsum;        // [ceil(m / 64)][n] or null
   const float* parts;
   int* exp_out;
@@ -321,8 +323,8 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a, const ConvertAr
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += v[j];
     if (a.out == nullptr) continue;
-    uint16_t* q = a.out + row * ((kSplit ? 2 : 1) * a.np) + col;
     if constexpr (kSplit) {
+      uint16_t* q = a.out + row * (2 * a.np) + (col / 32) * 64 + col % 32;
       u32x4 h, l;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -333,9 +335,9 @@ __global__ __launch_bounds__(256) void dz_kernel(const DzArgs a, const ConvertAr
         l[j] = l0 | (static_cast<uint32_t>(l1) << 16);
       }
       *reinterpret_cast<u32x4*>(q) = h;
-      if (a.lo) *reinterpret_cast<u32x4*>(q + a.np) = l;
+      *reinterpret_cast<u32x4*>(q + 32) = l;
     } else {
-      *reinterpret_cast<u32x4*>(q) = d0;  // dy as it lies (bf16)
+      *reinterpret_cast<u32x4*>(a.out + row * a.np + col) = pack_bf16(v);  // dy or 0 (bf16): exact
     }
   }
   if (a.bsum == nullptr) return;
@@ -408,11 +410,11 @@ __global__ __launch_bounds__(256) void dz_ragged_kernel(const DzArgs a, const Co
       if constexpr (kSplit) {
         uint16_t h, l;
         dz_split(v[j], e, h, l);
-        uint16_t* q = a.out + row * (2 * a.np) + col;
+        uint16_t* q = a.out + row * (2 * a.np) + (col / 32) * 64 + col % 32;
         q[0] = h;
-        if (a.lo) q[a.np] = l;
+        q[32] = l;
       } else if (a.out != nullptr) {
-        a.out[row * a.np + col] = bf16_bits(v[j]);  // dy itself (bf16): exact
+        a.out[row * a.np + col] = bf16_bits(v[j]);  // dy or 0 (bf16): exact
       }
     }
   }
@@ -487,11 +489,11 @@ struct BwdLayout {
 };
 BwdLayout bwd_layout(int64_t m, int64_t n, int64_t k, int dy_f32, int act) {
   BwdLayout l;
-  l.split = act != W4Q_ACT_NONE || dy_f32 != 0;
+  l.split = act == W4Q_ACT_GELU || act == W4Q_ACT_SILU || dy_f32 != 0;
   l.np = up32(n);
   l.mt = (m + kDzRows - 1) / kDzRows;
-  l.direct = !l.split && l.np == n;
-  l.px = lin_plan(m, k, l.np, 1, false);
+  l.direct = !l.split && act == W4Q_ACT_NONE && l.np == n;
+  l.px = lin_plan(m, k, l.np, l.split ? 2 : 1, false);
   l.pw = lin_plan(n, k, m, l.split ? 2 : 1, false);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -618,7 +620,7 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
   if (need || db != nullptr) {
     const bool whole = d_out % 8 == 0 && at16(z);
     const int64_t cols = whole ? (l.np + 255) / 256 : (l.np + 63) / 64;
-    const DzArgs a = {dy, dy_f32, z, act, m, d_out, l.np, need ? u16(l.dz) : nullptr, dw != nullptr ? 1 : 0, bsum, parts, exps, static_cast<int>(cols),
+    const DzArgs a = {dy, dy_f32, z, act, m, d_out, l.np, need ? u16(l.dz) : nullptr, bsum, parts, exps, static_cast<int>(cols),
                       static_cast<int>(cols * l.mt)};
     ConvertArgs c = {{x, w_hat}, {u16(l.x16), u16(l.w16)}, {m * d_in / 8, d_out * d_in / 8}, {0, 0}, exps};
     auto blocks = [](int64_t n8) { return static_cast<int>(n8 / 512 + 1 < 2048 ? n8 / 512 + 1 : 2048); };
@@ -649,7 +651,7 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
     g.K = static_cast<int>(l.np);
     g.kb = static_cast<int>(d_out);
     const EpiGrad e = {exps, l.split ? exps + 2 : nullptr, dx, 1, vec ? 1 : 0};
-    rc = l.split ? lin_product<1, true, false, true>(g, l.px, e, part, s) : lin_product<1, false, false, true>(g, l.px, e, part, s);
+    rc = l.split ? lin_product<2, true, false, true>(g, l.px, e, part, s) : lin_product<1, false, false, true>(g, l.px, e, part, s);
     if (rc != W4Q_OK) return rc;
   }
   if (dw != nullptr) {  // dW [d_out][d_in] = dz^T x: both across
@@ -659,7 +661,6 @@ int w4q_launch_linear_bwd(const uint16_t* x, int64_t m, const uint16_t* w_hat, i
     g.M = static_cast<int>(d_out);
     g.N = g.ldb = static_cast<int>(d_in);
     g.lda = ldz;
-    g.la = l.split ? static_cast<int>(l.np) : 0;
     g.K = g.ka = g.kb = static_cast<int>(m);
     const EpiGrad e = {exps, l.split ? exps + 1 : nullptr, dw, 0, vec ? 1 : 0};
     rc = l.split ? lin_product<2, true, true, true>(g, l.pw, e, part, s) : lin_product<1, false, true, true>(g, l.pw, e, part, s);

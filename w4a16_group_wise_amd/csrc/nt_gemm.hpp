@@ -75,8 +75,6 @@ struct NtArgs {
   int M, N, K;        // K a multiple of 32 unless both operands lie across
   int ka, kb;         // k rows that A, B really have, where they lie across (K up to the next 32 is zero)
   int lda, ldb;       // 16-bit values per row (both parts of a split operand), multiples of 8
-  int la, lb;         // split operands across: values from a row's hi part to its lo part where each lies in
-                      // one piece, 0 where the parts of 32 columns lie side by side
   int tm, tn;         // tiles along M and N
   int tri;            // 1: M == N and only tiles with row tile >= column tile
   int per_batch;      // tiles of one batch
@@ -127,24 +125,22 @@ struct NtOperand {
   static_assert(kLoads == 1 || kLoads == 2 || kLoads == 4, "loads per wave");
 
   // byte offset in memory of what lane `lane` brings with load u
-  // (lo: from a row's hi part to its lo part in values, 0: side by side; across only)
-  static __device__ __forceinline__ int load_off(int u, int lane, int ld, int lo) {
+  static __device__ __forceinline__ int load_off(int u, int lane, int ld) {
     constexpr int kChunks = kRow / 16, kRows = 64 / kChunks;  // chunks of a row, rows of a load
     const int r = u * kRows + lane / kChunks;
     const int c = (lane % kChunks) ^ (kAcross ? nt_tswz<kRow>(r) : nt_swz(r));
-    if (kAcross && P == 2 && lo != 0) return r * ld * 2 + 16 * ((c >> 3) * 4 + (c & 3)) + (c & 4 ? 2 * lo : 0);
     return r * ld * 2 + 16 * c;
   }
   // This wavefront's loads of stage s to `dst`: loads u0 .. u0 + kLoads - 1 of the tile whose first row
   // (along) or column (across) is r0, vo their load_off.  rows: the operand's rows (along) or k rows
   // (across).  !live: empty loads, which write zeros.
-  static __device__ __forceinline__ void issue(const uint16_t* base, int s, bool live, int r0, int rows, int ld, int lo, int K,
+  static __device__ __forceinline__ void issue(const uint16_t* base, int s, bool live, int r0, int rows, int ld, int K,
                                                uint32_t dst, int u0, int lane, const int (&vo)[kLoads]) {
     int64_t off;
     int bytes;
     if constexpr (kAcross) {
       const int left = rows - BK * s;
-      const int c0 = lo != 0 ? r0 : r0 * P;
+      const int c0 = r0 * P;
       off = static_cast<int64_t>(BK * s) * ld + c0;
       bytes = ((left < BK ? left : BK) * ld - c0) * 2;
     } else {
@@ -348,9 +344,9 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
 
   int avo[OpA::kLoads], bvo[OpB::kLoads], aro[C::MB], bro[C::NB];
 #pragma unroll
-  for (int q = 0; q < OpA::kLoads; ++q) avo[q] = OpA::load_off(wid * OpA::kLoads + q, lane, g.lda, g.la);
+  for (int q = 0; q < OpA::kLoads; ++q) avo[q] = OpA::load_off(wid * OpA::kLoads + q, lane, g.lda);
 #pragma unroll
-  for (int q = 0; q < OpB::kLoads; ++q) bvo[q] = OpB::load_off(wid * OpB::kLoads + q, lane, g.ldb, g.lb);
+  for (int q = 0; q < OpB::kLoads; ++q) bvo[q] = OpB::load_off(wid * OpB::kLoads + q, lane, g.ldb);
 #pragma unroll
   for (int i = 0; i < C::MB; ++i) aro[i] = OpA::read_off(wm * C::WM + 32 * i, lane);
 #pragma unroll
@@ -379,9 +375,9 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     // loads of stage s into buffer `buf` (past the range: empty)
     auto issue = [&](int s, int buf) {
       const uint32_t dst = lds0 + buf * C::kStage;
-      OpA::issue(abase, s, s < s1, m0, C::AT ? g.ka : g.M, g.lda, g.la, g.K, dst + wid * (OpA::kLoads * 1024), wid * OpA::kLoads,
+      OpA::issue(abase, s, s < s1, m0, C::AT ? g.ka : g.M, g.lda, g.K, dst + wid * (OpA::kLoads * 1024), wid * OpA::kLoads,
                  lane, avo);
-      OpB::issue(bbase, s, s < s1, n0, C::BT ? g.kb : g.N, g.ldb, g.lb, g.K, dst + OpA::kBytes + wid * (OpB::kLoads * 1024),
+      OpB::issue(bbase, s, s < s1, n0, C::BT ? g.kb : g.N, g.ldb, g.K, dst + OpA::kBytes + wid * (OpB::kLoads * 1024),
                  wid * OpB::kLoads, lane, bvo);
     };
 
@@ -577,14 +573,14 @@ __global__ __launch_bounds__(C::kThreads) void nt_tiny_kernel(const NtArgs g, co
   const uint16_t* bbase = g.b + batch * g.sb;
   int avo[OpA::kLoads], bvo[OpB::kLoads];
 #pragma unroll
-  for (int q = 0; q < OpA::kLoads; ++q) avo[q] = OpA::load_off(q, lane, g.lda, g.la);
+  for (int q = 0; q < OpA::kLoads; ++q) avo[q] = OpA::load_off(q, lane, g.lda);
 #pragma unroll
-  for (int q = 0; q < OpB::kLoads; ++q) bvo[q] = OpB::load_off(q, lane, g.ldb, g.lb);
+  for (int q = 0; q < OpB::kLoads; ++q) bvo[q] = OpB::load_off(q, lane, g.ldb);
   const int aro = OpA::read_off(0, lane), bro = OpB::read_off(0, lane);
   auto issue = [&](int s, int buf) {
     const uint32_t dst = lds0 + buf * C::kStage;
-    OpA::issue(abase, s, s < g.S, m0, C::AT ? g.ka : g.M, g.lda, g.la, g.K, dst, 0, lane, avo);
-    OpB::issue(bbase, s, s < g.S, n0, C::BT ? g.kb : g.N, g.ldb, g.lb, g.K, dst + OpA::kBytes, 0, lane, bvo);
+    OpA::issue(abase, s, s < g.S, m0, C::AT ? g.ka : g.M, g.lda, g.K, dst, 0, lane, avo);
+    OpB::issue(bbase, s, s < g.S, n0, C::BT ? g.kb : g.N, g.ldb, g.K, dst + OpA::kBytes, 0, lane, bvo);
   };
   // the first wavefront does the epilogue: what that reads is on its way before the operands
   typename Epi::Pre pre[NtStrip<C>::kPasses];
