@@ -25,6 +25,7 @@
 // and x, W and (without an activation, unless its rows need padding) dy are read as they are.
 #include "epilogue.hpp"
 #include "nt_gemm.hpp"
+#include "ragged.hpp"
 
 namespace w4q {
 namespace {
@@ -76,15 +77,12 @@ struct EpiLinear {
     }
     store8(y, o, y_dtype, v);
   }
-  // (addresses past the matrix are clamped rather than branched over, so that the loads overlap)
   __device__ __forceinline__ void load_rows(const NtArgs& g, int, int row, int col, float (&r)[8]) const {
 #pragma unroll
     for (int e = 0; e < 8; ++e) r[e] = 0.0f;
     if (ep.res == nullptr) return;
     int64_t o[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      o[e] = static_cast<int64_t>(row + e < g.M ? row + e : g.M - 1) * g.N + (col < g.N ? col : 0);
+    ragged8(row, g.M, col, g.N, [&](int e, int rr, int c) { o[e] = element_at(0, rr, g.M, c, g.N); });
     if (y_dtype == 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) r[e] = static_cast<const float*>(ep.res)[o[e]];

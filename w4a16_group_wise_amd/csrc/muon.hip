@@ -26,6 +26,7 @@
 #include "epilogue.hpp"
 #include "muon.hpp"
 #include "nt_gemm.hpp"
+#include "ragged.hpp"
 
 namespace w4q {
 namespace {
@@ -67,9 +68,7 @@ struct Split {
   int64_t stride;  // 16-bit values between batches (2 * rows * ld)
 
   // of the hi part of (row, col); the lo part is 32 further
-  __device__ __forceinline__ int64_t at(int batch, int64_t row, int col) const {
-    return batch * stride + row * (2 * ld) + (col >> 5) * 64 + (col & 31);
-  }
+  __device__ __forceinline__ int64_t at(int batch, int64_t row, int col) const { return split_at(batch, stride, row, ld, col); }
 };
 struct Pair8 {
   u32x4 h, l;
@@ -159,15 +158,13 @@ struct EpiLast {
       store8(out, o, out_dtype, v);
     }
   }
-  // (addresses past the matrix are clamped rather than branched over, so that the loads overlap)
   __device__ __forceinline__ void load_rows(const NtArgs& g, int batch, int row, int col, float (&t)[8]) const {
     uint16_t h[8], l[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint16_t* q = x.p + x.at(batch, row + e < g.M ? row + e : g.M - 1, col < x.ld ? col : 0);
+    ragged8(row, g.M, col, x.ld, [&](int e, int r, int c) {
+      const uint16_t* q = x.p + x.at(batch, r, c);
       h[e] = q[0];
       l[e] = q[32];
-    }
+    });
 #pragma unroll
     for (int e = 0; e < 8; ++e) t[e] = f16_bits_to_f32(h[e]) + f16_bits_to_f32(l[e]);
   }
@@ -179,8 +176,7 @@ struct EpiLast {
     for (int e = 0; e < 8; ++e) u[e] = __builtin_fmaf(alpha, t[e], beta * v[e]) * kSplitInv;
     if (w != nullptr) {
       float wv[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wv[e] = w[o + (row + e < g.M ? static_cast<int64_t>(e) * g.N : 0)];
+      ragged8(row, g.M, col, g.N, [&](int e, int r, int c) { wv[e] = w[element_at(batch, r, g.M, c, g.N)]; });
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[e] = wv[e] - lr * (scale * u[e] + wd * wv[e]);
     }
