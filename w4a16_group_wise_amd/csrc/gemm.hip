@@ -249,16 +249,28 @@ __device__ __forceinline__ void gstore_block(void* __restrict__ y, int y_dtype, 
                                              const f32x16& acc, int lane, const W4Epilogue& ep) {
   const int col = col0 + (lane & 31);
   if (col >= N) return;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int row = row0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-    if (row >= M) continue;
+  auto put = [&](int row, float v) {
+    if (row >= M) return;
     const int64_t o = (int64_t)row * N + col;
-    const float v = kEpi ? apply_epilogue(ep, acc[r], row, col, N, y_dtype) : acc[r];
+    if constexpr (kEpi) v = apply_epilogue(ep, v, row, col, N, y_dtype);
     if (y_dtype == 0)
       reinterpret_cast<float*>(y)[o] = v;
     else
       reinterpret_cast<uint16_t*>(y)[o] = f32_to_bf16_bits(v);
+  };
+  if constexpr (kEpi) {
+    // four values' code in a loop, the block turned by four each time: 128 copies of the activations would
+    // keep the callers' loops over their blocks from being unrolled, and the accumulators out of registers
+    f32x16 t = acc;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) put(row0 + 8 * q + 4 * (lane >> 5) + r, t[r]);
+      t = __builtin_shufflevector(t, t, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 0, 1, 2, 3);
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) put(row0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), acc[r]);
   }
 }
 
