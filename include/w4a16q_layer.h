@@ -109,7 +109,7 @@ int w4a16_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int w_mo
  *            far that A or b A + c A^2 exceeds 7.9 in norm (the operands' fixed-point range).
  *   steps 1 .. 64, eps >= 0 and finite.  (A zero matrix gives zeros; with eps = 0, NaN.)
  *   Operands of the products are held in 22 bits and summed in fp32: the error is that of fp32
- *   products.
+ *   products, also where ||G||_F is far below eps (a not 0: small singular values go by a s).
  *   workspace  newton_schulz_workspace_size bytes, 256-B aligned (W4Q_EINVAL if smaller or NULL).
  *   Limits: 1 <= rows, cols <= 131072, batch <= 65535, at most 2^30 steps of 32 k over all
  *   output tiles of a product and at most 2^24 - 16 tiles (W4Q_EUNSUPPORTED).

@@ -46,6 +46,8 @@ struct EpiLinear {
   int y_dtype;
   int vec;      // 8 columns of a row may be moved in 16-byte pieces
 
+  __device__ __forceinline__ int word(int) const { return 0; }
+  __device__ __forceinline__ const EpiLinear& with(int) const { return *this; }
   __device__ __forceinline__ bool whole() const { return vec != 0; }
   __device__ __forceinline__ Pre load(const NtArgs& g, int, int row, int col) const {
     Pre p = {};
@@ -126,6 +128,8 @@ struct EpiGrad {
   void* out;
   int out_dtype, vec;
 
+  __device__ __forceinline__ int word(int) const { return 0; }
+  __device__ __forceinline__ const EpiGrad& with(int) const { return *this; }
   __device__ __forceinline__ bool whole() const { return vec != 0; }
   __device__ __forceinline__ int exponent() const { return e0 != nullptr ? -(*e0 + *e1) : 0; }
   __device__ __forceinline__ Pre load(const NtArgs&, int, int, int) const { return Pre{exponent()}; }

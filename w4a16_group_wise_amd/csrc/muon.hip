@@ -14,6 +14,11 @@
 // 2^13: |X| <= 1.21, |A| <= 1.45, |B| <= 2.81 for the published coefficients (spectral bounds, so they
 // bound the entries), and 2^13 * 7.99 is fp16's largest value; other coefficients are checked against
 // these limits on the host.
+// Where ||U|| is below eps X0 is small, and a fixed point would leave it few bits.  So X is held times 2^e as
+// well: e_0 = E, one exponent for each matrix with 2^E ||X0||_F in [1/2, 1), and after s steps max(0, E - h_s),
+// h_s = ceil(s log2 g): a step multiplies singular values up to 1 by at most g = max |a + b t + c t^2| over
+// 0 <= t <= 1, so 2^e X stays within norm 1 until e is 0.  The epilogues take the power of two back (A) or
+// on (X); ordinary inputs have E = 0 and the bits they had without it.
 //
 // Work per step: A and A^2 are symmetric (tiles on and below the diagonal only, the others stored
 // mirrored), B X is whole: n^2 k + n^3 + 2 n^2 k flop, times three products.  Matrix-core bound from
@@ -31,8 +36,7 @@
 namespace w4q {
 namespace {
 
-constexpr float kSplitScale = 8192.0f;  // 2^13
-constexpr float kSplitInv = 1.0f / 8192.0f;
+constexpr float kSplitInv = 1.0f / 8192.0f;  // 2^-13
 
 // hi and lo of a scaled value (both RNE)
 __device__ __forceinline__ void split16(float v, uint16_t& h, uint16_t& l) {
@@ -85,7 +89,21 @@ __device__ __forceinline__ Pair8 load_pair(const Split& m, int batch, int row, i
   return Pair8{*reinterpret_cast<const u32x4*>(q), *reinterpret_cast<const u32x4*>(q + 32)};
 }
 
-// alpha * C + beta * acc, split, as the output (its rows' padding, where both terms are zero, included);
+// The power of two by which an epilogue's result is multiplied, from the matrix's exponent E: X comes with
+// e = max(0, E - from), `times` times (once, or twice in X X^T), and leaves with max(0, E - to)
+constexpr int kNoExponent = 1 << 30;  // as `to`: leaves without
+struct Exponent {
+  const int* e;  // E of each matrix, or null: no power of two
+  int from, times, to;
+  // a factor of the result times it, once per tile and in a scalar register (0 where a large negative power
+  // takes it below fp32's range: so is what it would multiply)
+  __device__ __forceinline__ float scaled(float v, int x) const {
+    const float f = __builtin_ldexpf(v, (x > to ? x - to : 0) - (x > from ? times * (x - from) : 0));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, f)));
+  }
+};
+
+// (alpha * C + beta * acc) 2^exponent, split, as the output (its rows' padding, where both terms are zero, included);
 // kSym: a symmetric result of which only the tiles on and below the diagonal are computed: the
 // others get the transposed values
 template <bool kSym>
@@ -96,7 +114,15 @@ struct EpiSplit {
   Split c;  // C term; c.p null: none
   float alpha, beta;
   Split o;
+  Exponent ex;
 
+  __device__ __forceinline__ int word(int batch) const { return ex.e != nullptr ? ex.e[batch] : 0; }
+  __device__ __forceinline__ EpiSplit with(int word) const {
+    EpiSplit e = *this;
+    e.alpha = ex.scaled(alpha, word);
+    e.beta = ex.scaled(beta, word);
+    return e;
+  }
   __device__ __forceinline__ bool whole() const { return true; }
   __device__ __forceinline__ void load_rows(const NtArgs&, int, int, int, float (&)[8]) const {}
   __device__ __forceinline__ void store_rows(const NtArgs&, int, int, int, const float (&)[8], const float (&)[8]) const {}
@@ -117,7 +143,7 @@ struct EpiSplit {
   }
 };
 
-// the last update: o = (alpha * X + beta * acc) 2^-13, stored as the result or applied to the weights
+// the last update: o = (alpha * X + beta * acc) 2^(-13 - e), stored as the result or applied to the weights
 struct EpiLast {
   static constexpr bool kMirror = false;
   static constexpr int kLoads = 1;
@@ -126,6 +152,7 @@ struct EpiLast {
     u32x4 w0, w1;
   };
   Split x;
+  Exponent ex;
   float alpha, beta;
   void* out;      // newton_schulz: [M][N] fp32 (dtype 0) or bf16 (1)
   int out_dtype;
@@ -133,6 +160,13 @@ struct EpiLast {
   float lr, scale, wd;
   int vec;        // 8 columns of a row may be moved in 16-byte pieces
 
+  __device__ __forceinline__ int word(int batch) const { return ex.e[batch]; }
+  __device__ __forceinline__ EpiLast with(int word) const {
+    EpiLast e = *this;
+    e.alpha = ex.scaled(alpha, word);
+    e.beta = ex.scaled(beta, word);
+    return e;
+  }
   __device__ __forceinline__ bool whole() const { return vec != 0; }
   __device__ __forceinline__ Pre load(const NtArgs& g, int batch, int row, int col) const {
     Pre p = {};
@@ -261,15 +295,21 @@ __global__ __launch_bounds__(256) void norm_kernel(const Source s, int64_t elems
   if (threadIdx.x == 0) sums[static_cast<int64_t>(batch) * parts + blockIdx.x] = acc;
 }
 
-// U / (||U|| + eps), split, [rows][ld] with the rows' ends zero; 8 values of a row per thread.  HBM
+// U / (||U|| + eps) 2^E, split, [rows][ld] with the rows' ends zero, and E; 8 values of a row per thread.  HBM
 // bound: one read of g (and m), 4 bytes written per value (12288x4096: 600 MB in 112 us).
 __global__ __launch_bounds__(256) void first_split_kernel(const Source s, int64_t rows, int cols, int parts, int vec,
-                                                          const double* __restrict__ sums, double eps, const Split o) {
+                                                          const double* __restrict__ sums, double eps, int* __restrict__ exps,
+                                                          const Split o) {
   const int batch = blockIdx.y;
   const double* sb = sums + static_cast<int64_t>(batch) * parts;
   double acc = 0.0;
   for (int i = threadIdx.x; i < parts; i += 256) acc += sb[i];
-  const double inv = 1.0 / (__builtin_sqrt(block_sum(acc)) + eps);
+  const double norm = __builtin_sqrt(block_sum(acc)), inv = 1.0 / (norm + eps);
+  int top = 0;
+  (void)__builtin_frexp(norm * inv, &top);  // ||X0|| < 2^top (a norm of 0, infinity or NaN: no exponent)
+  const int up = norm * inv > 0.0 && top < 0 ? -top : 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) exps[batch] = up;
+  const double factor = __builtin_ldexp(inv, 13 + up);
   const int64_t base = static_cast<int64_t>(batch) * rows * cols;
   const int per_row = o.ld / 8;
   const int64_t n8 = rows * per_row;
@@ -310,7 +350,7 @@ __global__ __launch_bounds__(256) void first_split_kernel(const Source s, int64_
     for (int e = 0; e < 8; ++e) {
       const float u = s.m == nullptr ? g[e] : s.nesterov ? __builtin_fmaf(s.mu, m[e], g[e]) : m[e];
       // the padding stays zero even where the norm is not finite
-      v[e] = col + e < cols ? static_cast<float>(static_cast<double>(u) * inv) * kSplitScale : 0.0f;
+      v[e] = col + e < cols ? static_cast<float>(static_cast<double>(u) * factor) : 0.0f;
     }
     store_pair(o, batch, row, col, v);
   }
@@ -346,7 +386,7 @@ struct NsLayout {
   int64_t n, np, ld;    // the smaller side, padded; X's row length (cols, padded)
   NtPlan gram, poly, upd;
   int parts;
-  size_t sums, x0, x1, aa, bb, part, total;  // byte offsets, end
+  size_t sums, exps, x0, x1, aa, bb, part, total;  // byte offsets, end
 };
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -370,6 +410,7 @@ NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
     return at;
   };
   l.sums = take(sizeof(double) * batch * l.parts);
+  l.exps = take(sizeof(int) * batch);
   l.x0 = take(x_bytes);
   l.x1 = take(x_bytes);
   l.aa = take(n_bytes);
@@ -437,6 +478,14 @@ bool w4q_ns_coeffs_ok(int steps, double a, double b, double c) {
   return true;
 }
 
+// h_s of the exponents (at the top): the bits by which singular values up to 1 can grow in s steps
+static int growth_bits(int s, double a, double b, double c) {
+  double g = __builtin_fmax(1.0, __builtin_fmax(__builtin_fabs(a), __builtin_fabs(a + b + c)));
+  const double t = c != 0.0 ? -b / (2.0 * c) : 0.0;  // where a + b t + c t^2 turns
+  if (t > 0.0 && t < 1.0) g = __builtin_fmax(g, __builtin_fabs(a + t * (b + c * t)));
+  return static_cast<int>(__builtin_ceil(s * __builtin_log2(g)));
+}
+
 // newton_schulz: g -> out.  muon_step: m != null, w updated in place.
 int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64_t cols, int steps, float a, float b,
                   float c, double eps, void* out, int out_dtype, float* m, float mu, int nesterov, float* w, float lr,
@@ -449,6 +498,7 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
   const NsLayout l = ns_layout(batch, rows, cols);
   uint8_t* base = static_cast<uint8_t*>(ws);
   double* sums = reinterpret_cast<double*>(base + l.sums);
+  int* exps = reinterpret_cast<int*>(base + l.exps);
   auto split = [&](size_t off, int64_t m_rows, int64_t ld) {
     return Split{reinterpret_cast<uint16_t*>(base + off), static_cast<int>(ld), 2 * m_rows * ld};
   };
@@ -465,7 +515,7 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
   if (rc != W4Q_OK) return rc;
   const int64_t blocks = (rows * l.ld / 8 + 255) / 256;
   hipLaunchKernelGGL(first_split_kernel, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), static_cast<unsigned>(batch)),
-                     dim3(256), 0, s, src, rows, static_cast<int>(cols), l.parts, vec ? 1 : 0, sums, eps, x[0]);
+                     dim3(256), 0, s, src, rows, static_cast<int>(cols), l.parts, vec ? 1 : 0, sums, eps, exps, x[0]);
   rc = w4q_launch_status();
 
   auto operand = [](const Split& m, const uint16_t*& p, int64_t& stride, int& ld) {
@@ -476,6 +526,7 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
   int cur = 0;
   for (int i = 0; i < steps && rc == W4Q_OK; ++i, cur ^= 1) {
     const Split& X = x[cur];
+    const int h = growth_bits(i, a, b, c), next = growth_bits(i + 1, a, b, c);
     // A = X X^T (Y^T Y)
     NtArgs ga = {};
     operand(X, ga.a, ga.sa, ga.lda);
@@ -486,6 +537,7 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
     EpiSplit<true> e = {};
     e.beta = kSplitInv;
     e.o = A;
+    e.ex = {exps, h, 2, kNoExponent};
     rc = l.wide ? ns_product<false, false>(ga, l.gram, 1, e, part, s) : ns_product<true, true>(ga, l.gram, 1, e, part, s);
     if (rc != W4Q_OK) break;
     // B = b A + c A A
@@ -498,6 +550,7 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
     e.alpha = b;
     e.beta = c * kSplitInv;
     e.o = B;
+    e.ex = {};
     if ((rc = ns_product<false, false>(gb, l.poly, 1, e, part, s)) != W4Q_OK) break;
     // X <- a X + B X (Y <- a Y + Y B)
     NtArgs gx = {};
@@ -513,10 +566,12 @@ int w4q_launch_ns(const void* g, int g_dtype, int64_t batch, int64_t rows, int64
       u.alpha = a;
       u.beta = kSplitInv;
       u.o = x[cur ^ 1];
+      u.ex = {exps, h, 1, next};
       rc = l.wide ? ns_product<false, true>(gx, l.upd, 0, u, part, s) : ns_product<false, false>(gx, l.upd, 0, u, part, s);
     } else {
       EpiLast u = {};
       u.x = X;
+      u.ex = {exps, h, 1, kNoExponent};
       u.alpha = a;
       u.beta = kSplitInv;
       u.out = out;

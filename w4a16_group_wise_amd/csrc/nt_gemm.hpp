@@ -225,6 +225,8 @@ __device__ __forceinline__ int64_t nt_part_off(int w, int blk, int q, int lane) 
 // ---------------------------------------------------------------------------- epilogue strips
 // A strip is 32 rows x WN columns of a wavefront's tile.  Lane l takes 8 columns from 8 (l % (WN / 8)) of
 // rows l / (WN / 8) + kRows i.  The functor gives, for 8 columns of one row:
+//   int word(batch)                                  a word of the tile's matrix, read before its product
+//   Epi with(word)                                   the functor for that tile
 //   Pre load(g, batch, row, col)                     what the epilogue reads there.  kLoads: 2 the next
 //                                                    strip's before a strip is stored, 1 after, 0 a
 //                                                    pass ahead, in a loop (for long epilogues, whose
@@ -326,7 +328,7 @@ __device__ __forceinline__ void nt_strip_store(const NtArgs& g, const Epi& epi, 
 }
 
 template <class C, class Epi>
-__global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const Epi epi) {
+__global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const Epi args) {
   using OpA = typename C::OpA;
   using OpB = typename C::OpB;
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
@@ -371,6 +373,7 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     const int m0 = ti * C::BM, n0 = tj * C::BN;
     const uint16_t* abase = g.a + batch * g.sa;
     const uint16_t* bbase = g.b + batch * g.sb;
+    const int word = args.word(batch);
 
     // loads of stage s into buffer `buf` (past the range: empty)
     auto issue = [&](int s, int buf) {
@@ -463,6 +466,7 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
     sync(std::integral_constant<int, 0>{});
 
     if (s0 == 0 && s1 == g.S) {
+      const Epi& epi = args.with(word);
       float* strip = reinterpret_cast<float*>(lds + wid * (C::kLds / C::kWaves));
       const int row0 = m0 + wm * C::WM, col0 = n0 + wn * C::WN;
       constexpr int kSets = Epi::kLoads == 2 ? 2 : 1;
@@ -496,7 +500,7 @@ __global__ __launch_bounds__(C::kThreads) void nt_kernel(const NtArgs g, const E
 // Tiles whose stages were spread over several workgroups: the partial tiles summed in k order,
 // then the epilogue.  One wavefront per strip of 32 rows x WN columns.
 template <class C, class Epi>
-__global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi epi) {
+__global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi args) {
   __shared__ __attribute__((aligned(16))) float strip[32 * C::kPitch];
   constexpr int kStrips = C::kWaves * C::MB;  // strips of a tile
   int t = static_cast<int>(blockIdx.x) / kStrips;
@@ -512,6 +516,7 @@ __global__ __launch_bounds__(64) void nt_fixup_kernel(const NtArgs g, const Epi 
   nt_tile(g, t, batch, ti, tj);
   const int row0 = ti * C::BM + (wid / C::kWavesN) * C::WM + 32 * i;
   const int col0 = tj * C::BN + (wid % C::kWavesN) * C::WN;
+  const Epi& epi = args.with(args.word(batch));
   typename Epi::Pre pre[NtStrip<C>::kPasses];
   if (Epi::kLoads != 0) nt_strip_load<C>(g, epi, batch, row0, col0, lane, pre);
   f32x16 v[C::NB];
@@ -556,7 +561,7 @@ struct NtTinyCfg {
 };
 
 template <class C, class Epi>
-__global__ __launch_bounds__(C::kThreads) void nt_tiny_kernel(const NtArgs g, const Epi epi) {
+__global__ __launch_bounds__(C::kThreads) void nt_tiny_kernel(const NtArgs g, const Epi args) {
   using OpA = typename C::OpA;
   using OpB = typename C::OpB;
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
@@ -583,8 +588,9 @@ __global__ __launch_bounds__(C::kThreads) void nt_tiny_kernel(const NtArgs g, co
     OpB::issue(bbase, s, s < g.S, n0, C::BT ? g.kb : g.N, g.ldb, g.K, dst + OpA::kBytes, 0, lane, bvo);
   };
   // the first wavefront does the epilogue: what that reads is on its way before the operands
+  const int word = args.word(batch);
   typename Epi::Pre pre[NtStrip<C>::kPasses];
-  if (wid == 0 && Epi::kLoads != 0) nt_strip_load<C>(g, epi, batch, m0, n0, lane, pre);
+  if (wid == 0 && Epi::kLoads != 0) nt_strip_load<C>(g, args, batch, m0, n0, lane, pre);
   asm volatile("" ::: "memory");
   f32x16 acc[1];
 #pragma unroll
@@ -625,6 +631,7 @@ __global__ __launch_bounds__(C::kThreads) void nt_tiny_kernel(const NtArgs g, co
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing is on its way to the buffers
   asm volatile("" ::: "memory");
   nt_strip_write<C>(acc, lane, reinterpret_cast<float*>(mine));
+  const Epi& epi = args.with(word);
   __syncthreads();
   float* strip = reinterpret_cast<float*>(lds);
   constexpr int kStride = 2 * C::kStage / 4;  // floats between the wavefronts' strips
