@@ -67,7 +67,8 @@ int lsq_linear_fwd_workspace_size(int64_t m, int64_t d_out, int64_t d_in, size_t
  *   z          bf16 [m][d_out]; NULL only with W4Q_ACT_NONE.
  *   grad_x, grad_w_hat, grad_bias   outputs; each may be NULL, not all three.
  *   dz enters both products in 22 bits (with bf16 grad_y and W4Q_ACT_NONE or W4Q_ACT_RELU: as it
- *   is), relative to values within 2^-24 of the largest |grad_y|.
+ *   is) down to 2^-16 of the largest |grad_y|, and off by at most 2^-38 of that largest below; x and w_hat
+ *   then enter as they are down to 2^-30 of their largest, and off by at most 2^-38 of it below.
  *   workspace  lsq_linear_bwd_workspace_size bytes, 256-B aligned (W4Q_EINVAL if smaller or NULL).
  *   Limits: as for the forward, with m <= 4194240, d_out <= 2^20 and at most 2^24 - 2^13 blocks of
  *   64 x 64 in dz (W4Q_EUNSUPPORTED).

@@ -15,9 +15,11 @@
 // Backward: the products read their operands across their rows where they lie so (dx: W; dW: dz and
 // x), so nothing is transposed in memory.  dW and dbias are fp32 results, so dz may not be rounded
 // to bf16: with gelu and silu (or fp32 dy) dz is held as two fp16 parts, 22 bits, and dW = lo x +
-// hi x.  A bf16 value has 8 bits, so x and W are exact in fp16 once a power of two brings their
-// largest value to 2^14 (values below 2^-32 of the largest lose bits, an absolute error of 2^-40 of
-// it); the exponents come from one maximum over each tensor and are taken back in the epilogue.
+// hi x.  The parts are of dz 2^e, which brings the largest |dy| into [2^13, 2^14), and lo's last step is
+// 2^-24: below 2^-16 of that largest dz loses bits, an absolute error of at most 2^-38 of it.  A bf16 value has
+// 8 bits, so x and W are exact in fp16 times the power of two that brings their largest there (below 2^-30 of
+// it they lose bits, at most 2^-38 of it); the exponents come from one maximum over each tensor and are
+// taken back in the epilogue.
 // dx takes both parts too: with the hi part alone (11 bits) one result in 25 was another bf16 value
 // than the sum's own rounding; the second product costs a quarter of the call (8192x12288x4096 2199 ->
 // 2710 us).
@@ -31,7 +33,6 @@ namespace w4q {
 namespace {
 
 constexpr int kAmaxBlocks = 1024; // partial maxima of one tensor
-constexpr float kDactMax = 1.13f; // |act'| <= 1.1290 (gelu), 1.0999 (silu), 1 (relu, none)
 
 // ------------------------------------------------------------------------------ epilogues
 struct EpiLinear {
@@ -201,7 +202,8 @@ __global__ __launch_bounds__(256) void amax_kernel(const AmaxArgs a, float* __re
 }
 
 // The exponent e of a tensor's scale from its partial maxima (all 256 threads of the workgroup):
-// amax * 2^e in [2^13, 2^14), so kDactMax * amax * 2^e < 2^15.  e = 0 for a tensor of zeros.
+// amax * 2^e in [2^13, 2^14), and dz 2^e below 2^15: |act'| <= 1.1290 (gelu), 1.0999 (silu), 1 (relu,
+// none).  e = 0 for a tensor of zeros.
 __device__ __forceinline__ int scale_exp(const float* __restrict__ parts) {
   __shared__ float red[4];
   float m = 0.0f;
@@ -219,7 +221,7 @@ __device__ __forceinline__ int scale_exp(const float* __restrict__ parts) {
   return 14 - e;
 }
 
-// x and W as fp16 times the power of two of their maxima (exact: 8 significant bits), whose
+// x and W as fp16 times the power of two of their maxima (exact within 2^-30 of those: 8 bits), whose
 // exponents go to exps[1] and exps[2].  HBM bound: 4 B per value.
 struct ConvertArgs {
   const uint16_t* src[2];
