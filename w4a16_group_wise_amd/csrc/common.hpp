@@ -171,7 +171,8 @@ __device__ __forceinline__ int lane_id() { return __builtin_amdgcn_mbcnt_hi(~0u,
 // Epilogue of a layer product (epilogue.hpp): act(sum + bias) + residual
 struct W4Epilogue {
   const float* bias;  // [N] or null
-  const void* res;    // [M][N] of the output's type, or null
+  const void* res;    // [M][N] of the output's type, or null; may be the output itself, which therefore
+                      // no kernel with an epilogue declares __restrict__
   int act;            // w4q_act
 };
 

@@ -57,7 +57,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_group_kernel(const uint16_t
                                                           const uint8_t* __restrict__ packed,
                                                           const uint16_t* __restrict__ s16,
                                                           int64_t N, int64_t K,
-                                                          void* __restrict__ y, int y_dtype,
+                                                          void* y, int y_dtype,
                                                           int64_t gn, int64_t tiles, int64_t per_xcd,
                                                           const W4Epilogue ep) {
   constexpr int NT = 64 * WM * WN;  // threads
@@ -245,7 +245,7 @@ __device__ __forceinline__ int64_t gpart_off(int w, int i, int a, int lane) {
 
 // Store one 32x32 accumulator block (rows row0.., columns col0..) of y, through the epilogue if kEpi.
 template <bool kEpi>
-__device__ __forceinline__ void gstore_block(void* __restrict__ y, int y_dtype, int M, int N, int row0, int col0,
+__device__ __forceinline__ void gstore_block(void* y, int y_dtype, int M, int N, int row0, int col0,
                                              const f32x16& acc, int lane, const W4Epilogue& ep) {
   const int col = col0 + (lane & 31);
   if (col >= N) return;
@@ -283,7 +283,7 @@ template <bool kSplit, bool kEpi>
 __global__ __launch_bounds__(kGThreads, 1) void gemm_dq_kernel(const uint16_t* __restrict__ x, int M,
                                                                 const uint8_t* __restrict__ packed,
                                                                 const uint16_t* __restrict__ s16, int N, int K,
-                                                                void* __restrict__ y, int y_dtype, int tn_count,
+                                                                void* y, int y_dtype, int tn_count,
                                                                 int total, int chunk, int nblk, int per_xcd,
                                                                 float* __restrict__ ws, const W4Epilogue ep) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kGemmLds];
@@ -513,7 +513,7 @@ __global__ __launch_bounds__(kGThreads, 1) void gemm_dq_kernel(const uint16_t* _
 // their K ranges, then store.  One workgroup of 8 wavefronts per (tile, block row i); wavefront
 // w sums its own block (rows 32 i.., columns 32 w..).
 template <bool kEpi>
-__global__ __launch_bounds__(kGThreads) void gemm_fixup_kernel(void* __restrict__ y, int y_dtype, int M, int N,
+__global__ __launch_bounds__(kGThreads) void gemm_fixup_kernel(void* y, int y_dtype, int M, int N,
                                                                int G, int tn_count, int chunk,
                                                                const float* __restrict__ ws, const W4Epilogue ep) {
   const int t = blockIdx.x >> 3;

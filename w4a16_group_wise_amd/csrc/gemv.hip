@@ -266,7 +266,7 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_mma_kernel(const uint16_t* _
                                                                   const uint8_t* __restrict__ packed,
                                                                   const uint16_t* __restrict__ s16,
                                                                   int64_t d_out, int64_t d_in,
-                                                                  void* __restrict__ y, int y_dtype, const W4Epilogue ep) {
+                                                                  void* y, int y_dtype, const W4Epilogue ep) {
   __shared__ float part[kWaves][kMmaTiles][4][64];
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
