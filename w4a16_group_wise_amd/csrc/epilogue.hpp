@@ -8,6 +8,15 @@
 namespace w4q {
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
+// a product's value as bf16: with an epilogue it may be any NaN (a bias's), which the rounding by an integer
+// addition of common.hpp would carry into 0 where all its bits are set
+template <bool kEpi>
+__device__ __forceinline__ uint16_t product_bf16(float v) {
+  if constexpr (kEpi)
+    return bf16_bits(v);
+  else
+    return f32_to_bf16_bits(v);
+}
 __device__ __forceinline__ float bf16_val(uint16_t b) { return __builtin_bit_cast(float, static_cast<uint32_t>(b) << 16); }
 
 // 1 / (1 + exp(-z)) by the hardware's 2^x and reciprocal (each within one last place): the exponent's

@@ -190,7 +190,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_group_kernel(const uint16_t
           if (y_dtype == 0)
             reinterpret_cast<float*>(y)[row * N + col] = v;
           else
-            reinterpret_cast<uint16_t*>(y)[row * N + col] = f32_to_bf16_bits(v);
+            reinterpret_cast<uint16_t*>(y)[row * N + col] = product_bf16<kEpi>(v);
         }
       }
     }
@@ -256,7 +256,7 @@ __device__ __forceinline__ void gstore_block(void* y, int y_dtype, int M, int N,
     if (y_dtype == 0)
       reinterpret_cast<float*>(y)[o] = v;
     else
-      reinterpret_cast<uint16_t*>(y)[o] = f32_to_bf16_bits(v);
+      reinterpret_cast<uint16_t*>(y)[o] = product_bf16<kEpi>(v);
   };
   if constexpr (kEpi) {
     // four values' code in a loop, the block turned by four each time: 128 copies of the activations would

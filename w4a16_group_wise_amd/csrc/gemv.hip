@@ -405,7 +405,7 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_mma_kernel(const uint16_t* _
       if (y_dtype == 0)
         reinterpret_cast<float*>(y)[m * d_out + n] = v;
       else
-        reinterpret_cast<uint16_t*>(y)[m * d_out + n] = f32_to_bf16_bits(v);
+        reinterpret_cast<uint16_t*>(y)[m * d_out + n] = product_bf16<kEpi>(v);
     }
   }
 }
@@ -613,7 +613,7 @@ __global__ __launch_bounds__(stream_threads<kLut>()) void gemv_stream_kernel(con
     if (ydt == 0)
       global_ptr(reinterpret_cast<float*>(y))[row] = v;
     else
-      global_ptr(reinterpret_cast<uint16_t*>(y))[row] = f32_to_bf16_bits(v);
+      global_ptr(reinterpret_cast<uint16_t*>(y))[row] = product_bf16<kEpi>(v);
   };
   // reduce the lane partials of each row of `item` (fixed order), store, and restart the
   // accumulators
