@@ -45,7 +45,7 @@ enum w4q_act { W4Q_ACT_NONE = 0, W4Q_ACT_RELU = 1, W4Q_ACT_GELU = 2, W4Q_ACT_SIL
  *   workspace NULL with 0 bytes, or 256-B aligned scratch; with less than the query's size no
  *             output tile is split over workgroups (same arithmetic up to the summation order).
  *   Limits: m, d_out < 2^30, d_in <= 2^21, at most 2^30 steps of 32 k over all 64 x 64 output
- *   tiles, and at most 2^24 - 16 of the tiles (W4Q_EUNSUPPORTED).
+ *   tiles, and at most 2^24 - 16 of the tiles; with w, d_out * d_in <= 2^35 - 2^11 (W4Q_EUNSUPPORTED).
  */
 int lsq_linear_fwd(const uint16_t* x, int64_t m, const float* w, const float* scale, int64_t d_out,
                    int64_t d_in, const float* bias, int act, const void* residual, uint16_t* w_hat,

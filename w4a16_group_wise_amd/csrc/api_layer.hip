@@ -58,6 +58,7 @@ int lsq_linear_fwd(const uint16_t* x, int64_t m, const float* w, const float* sc
   int rc = check_layer(m, d_out, d_in);
   if (rc != W4Q_OK) return rc;
   if (!w4q_linear_fits(m, d_out, d_in, false)) return W4Q_EUNSUPPORTED;
+  if (w != nullptr && !w4q_lsq_fwd16_fits(d_out, d_in)) return W4Q_EUNSUPPORTED;
   if (!aligned(x, 16) || !aligned(w_hat, 16) || (w && !aligned(w, 16)) || (scale && !aligned(scale, 4)) ||
       (bias && !aligned(bias, 4)) || (z && !aligned(z, 2)) || !aligned(y, width(y_dtype)) ||
       (residual && !aligned(residual, width(y_dtype))))

@@ -225,6 +225,7 @@ int w4q_launch_gptq(const float* w, int64_t d_out, int64_t d_in, const float* h,
 int w4q_launch_gemm(const uint16_t* x, int64_t m, const uint8_t* packed, const uint16_t* s16,
                     int64_t d_out, int64_t d_in, void* y, int y_dtype, int w_mode, void* ws,
                     size_t ws_bytes, hipStream_t s, const w4q::W4Epilogue* ep = nullptr);
+bool w4q_lsq_fwd16_fits(int64_t d_out, int64_t d_in);
 int w4q_launch_lsq_fwd16(const float* w, const float* scale, int64_t d_out, int64_t d_in,
                          uint16_t* w_hat, hipStream_t s);
 bool w4q_linear_fits(int64_t m, int64_t d_out, int64_t d_in, bool backward);

@@ -276,6 +276,9 @@ int w4q_launch_lsq_fwd(const float* w, const float* scale, int64_t d_out, int64_
   return w4q_launch_status();
 }
 
+// a launch's threads, 8 weights each in whole workgroups, count below 2^32
+bool w4q_lsq_fwd16_fits(int64_t d_out, int64_t d_in) { return d_out * d_in <= (int64_t(1) << 35) - kPer * kThreads; }
+
 int w4q_launch_lsq_fwd16(const float* w, const float* scale, int64_t d_out, int64_t d_in,
                          uint16_t* w_hat, hipStream_t s) {
   const int64_t n8 = d_out * d_in / kPer;
