@@ -563,6 +563,14 @@ def w4a16_linear(x: torch.Tensor, packed: torch.Tensor, scale_f16: torch.Tensor,
     return y
 
 
+def _steps(steps) -> int:
+    """steps as the library's int: refused where it is no whole number or would wrap around."""
+    n = int(steps)
+    if n != steps or not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"steps must be a whole number of 1 to 64, got {steps}")
+    return n
+
+
 def _matrices(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     """(batch, rows, cols) of a [rows][cols] or [batch][rows][cols] tensor."""
     if t.dim() not in (2, 3):
@@ -591,7 +599,7 @@ def newton_schulz(g: torch.Tensor, *, steps: int = 5, coeffs=NS_COEFFS, eps: flo
             _no_overlap((((y, "out"), (g, "g")),))
         wp, wb, _keep = _scratch("newton_schulz_workspace_size", (b, r, c), g.device, workspace)
         check("newton_schulz", lib().newton_schulz(
-            g.data_ptr(), gdt, b, r, c, int(steps), (ctypes.c_float * 3)(*coeffs), float(eps), y.data_ptr(), o, wp, wb,
+            g.data_ptr(), gdt, b, r, c, _steps(steps), (ctypes.c_float * 3)(*coeffs), float(eps), y.data_ptr(), o, wp, wb,
             _stream(g)))
     return y
 
@@ -613,7 +621,7 @@ def muon_step(w: torch.Tensor, grad: torch.Tensor, m: torch.Tensor, *, lr: float
     if update_scale is None:
         update_scale = max(1.0, r / max(c, 1)) ** 0.5
     hp = MuonParams(lr, momentum, weight_decay, update_scale, (ctypes.c_float * 3)(*coeffs), 1 if nesterov else 0,
-                    int(steps), float(eps))
+                    _steps(steps), float(eps))
     with _OnDevice(w.device):
         wp, wb, _keep = _scratch("newton_schulz_workspace_size", (b, r, c), w.device, workspace)
         check("muon_step", lib().muon_step(w.data_ptr(), grad.data_ptr(), m.data_ptr(), b, r, c, ctypes.byref(hp), wp,
