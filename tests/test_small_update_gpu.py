@@ -36,7 +36,7 @@ def near_fp32(o, g, what, **kw):
     assert bool((err <= bound).all()), f"{what}: {(err / bound).max():.3g} of the bound, {(err / norm).max():.3g} of the result"
 
 
-SHAPES = [(1, 70, 90), (1, 256, 512), (1, 300, 131), (2, 130, 777), (1, 1100, 1300)]
+SHAPES = [(1, 40, 200), (3, 90, 33), (1, 70, 90), (1, 256, 512), (1, 300, 131), (2, 130, 777), (1, 1100, 1300)]
 
 
 @pytest.mark.parametrize("b,r,c", SHAPES)
