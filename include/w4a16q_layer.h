@@ -5,7 +5,8 @@
  *
  * The chain of one training step of a linear:
  *   lsq_linear_fwd -> (loss) -> lsq_linear_bwd -> lsq_bwd -> muon_step (or lsq_adam_step)
- * and after training: quant_pack -> w4a16_linear.
+ * (muon_step steps the weights alone: the step of Delta from lsq_bwd's gradient is the caller's, where
+ * lsq_adam_step steps both) and after training: quant_pack -> w4a16_linear.
  *
  * The conventions of w4a16q.h hold (device memory, row-major and contiguous, work enqueued on
  * `stream`, nothing allocated or synchronised, argument errors reported before anything is

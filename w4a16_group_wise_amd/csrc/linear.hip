@@ -254,7 +254,7 @@ __device__ __forceinline__ void convert_part(const ConvertArgs& a, int t, int bl
 // activation or relu: exact); and column sums over the workgroup's 64 rows for dbias.  A thread has
 // 8 columns of a row, a workgroup 256 columns x 64 rows, 8 rows at a time.  HBM bound: dy and z read,
 // 4 (2) B written per value (8192x12288x4096
-// with the conversions: 1.14 GB in 198 us).
+// with the conversions: 1.14 GB in 208 us).
 constexpr int kDzRows = 64;
 struct DzArgs {
   const void* dy;

@@ -37,7 +37,7 @@
 //
 // Bound by the matrix cores at the clocks they hold under such a load (1.4 to 1.7 GHz) and by the operands'
 // way from L2 to LDS.  Measured with the epilogues: 1 x 1 parts 8192x12288x4096 1.25 PFLOP/s, 2 x 1 across
-// 1.24, 2 x 2 12288x4096x4096 1.24 to 1.3; the main loop alone reaches 1.4 (the library's plain product of 8192
+// 1.24, along and across 1.25, 2 x 2 12288x4096x4096 1.24 to 1.3; the main loop alone reaches 1.4 (the library's plain product of 8192
 // cubed: 1.52).
 //
 // Work split: one tile per workgroup; or as many whole tiles as each of the workgroups that fit the
