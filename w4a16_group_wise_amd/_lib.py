@@ -112,6 +112,7 @@ BLOCK_SIGNATURES = {
     "grad_norm_workspace_size": (_INT, [_I64, _P]),
 }
 FP8_BLOCK = 128
+FP8_SHORT = 256
 W4Q_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 

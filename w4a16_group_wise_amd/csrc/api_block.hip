@@ -9,6 +9,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 inline bool dtype_ok(int t) { return t == 0 || t == 1; }
 inline bool flag_ok(int t) { return t == 0 || t == 1; }
 inline uintptr_t width(int dtype) { return dtype == 0 ? 4 : 2; }
+inline bool gemm_dtype_ok(int t) { return dtype_ok(t) || t == (1 | W4Q_FP8_SHORT); }
 inline bool finite_value(float v) { return __builtin_isfinite(v); }
 
 // scratch of exactly or more than `need` bytes (0: none is needed)
@@ -119,7 +120,7 @@ int fp8_quant(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt, i
 }
 
 int fp8_gemm_workspace_size(int64_t m, int64_t n, int64_t k, int y_dtype, size_t* bytes) {
-  if (!bytes || !dtype_ok(y_dtype)) return W4Q_EINVAL;
+  if (!bytes || !gemm_dtype_ok(y_dtype)) return W4Q_EINVAL;
   const int rc = check_gemm(m, n, k);
   if (rc != W4Q_OK) return rc;
   *bytes = w4q_fp8_gemm_workspace(m, n, k, y_dtype);
@@ -130,7 +131,7 @@ int fp8_gemm(const uint8_t* a, int a_fmt, const float* a_scale, int64_t m, const
              int b_square, int64_t n, int64_t k, const float* bias, int act, const void* residual, void* y, int y_dtype,
              void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (!a || !a_scale || !b || !b_scale || !y || !flag_ok(a_fmt) || !flag_ok(b_fmt) || !flag_ok(b_square) ||
-      act < W4Q_ACT_NONE || act > W4Q_ACT_SILU || !dtype_ok(y_dtype))
+      act < W4Q_ACT_NONE || act > W4Q_ACT_SILU || !gemm_dtype_ok(y_dtype))
     return W4Q_EINVAL;
   int rc = check_gemm(m, n, k);
   if (rc != W4Q_OK) return rc;

@@ -5,13 +5,14 @@
 //
 // Two kinds of product.  The matrix cores' 8-bit products are exact, but they add them in groups of 8 consecutive k
 // aligned to the group's largest exponent, and what lies below 2^-13 of that is cut off (measured bit by bit on both
-// 8-bit forms; between groups and with the fp32 operand the sums are fp32's).  A bf16 result does not show it: the
-// cut is below 7 2^-13 of a group's largest product, 5e-5 of the result where the values spread over several
-// powers of two, and its own rounding is 2^-9 of it.  So:
-//   bf16 y: v_mfma_f32_16x16x128_f8f6f4 on the codes as they lie (kWide false).
-//   fp32 y (weight gradients, accumulated): the codes as bf16 values (exact: 3 or 2 bits behind the point) and
-//     v_mfma_f32_16x16x32_bf16 on them, whose products and sums are fp32's (kWide); written to the workspace once, or
-//     up to 64 rows made in registers, where HBM leaves the time.
+// 8-bit forms; between groups and with the fp32 operand the sums are fp32's).  So:
+//   the codes as bf16 values (exact: 3 or 2 bits behind the point) and v_mfma_f32_16x16x32_bf16 on them, whose products
+//     and sums are fp32's (kWide); written to the workspace once, or up to 64 rows made in registers, where HBM leaves the
+//     time.
+//   bf16 y with W4Q_FP8_SHORT, where the caller asks for it: v_mfma_f32_16x16x128_f8f6f4 on the codes as they lie (kWide
+//     false), at twice the rate.  The cut is below 7 2^-13 of a group's largest product; where the values spread over
+//     several powers of two it comes to some 3e-5 of the result, and one bf16 result in 200 is the neighbour of the one
+//     that fp32 sums give.
 //
 // A block's products are summed from zero, then scaled and added to the fp32 sums by the vector units, which have the
 // matrix cores' time for it: 16 fused multiply-adds for 128 clocks.  b's rows are the rows of the matrix
@@ -23,11 +24,12 @@
 // LDS and the fragments are nt_gemm.hpp's for 64 16-bit values (which 16-byte pieces of k a lane holds does not
 // matter as long as both operands agree).  The stage's scales travel beside them, 4 bytes a lane.
 //
-// What bounds it: at 12288x4096x8192 codes take 371 us (2.2 PFLOP/s; the clock under this load, and the operands' way
-// through the L2: with loads from the LDS alone the same products take 285).  fp32 results take 881 with a scale for each
-// row of b, 80 of them the bf16 copies at HBM's rate (the products at 1.03 PFLOP/s: the scaling of each 64 k takes the vector
-// units as long), 815 with square blocks.  Few rows: HBM, 1x4096x12288 12.1 us (4.2 TB/s with the launch), 13x12288x4096
-// 15.5.
+// What bounds it, square scales: 8192x12288x4096 743 us (1.11 PFLOP/s; the scaling of each 64 k takes the vector units
+// nearly as long as the matrix cores their products), of which about 80 for the bf16 copies at HBM's rate; short sums 405 to 455
+// (the clock under this load, and the operands' way through the L2: at 12288x4096x8192 they take 371, with loads from the LDS
+// alone 285).  With a scale for each row of b 12288x4096x8192 takes 881, with square blocks 815.  65 to 2048 rows: the copies
+// of b and two launches, 200 rows of 4096x4096 38 us, short sums 16.  Few rows: HBM, 1x4096x12288 14 us,
+// 13x12288x4096 16.
 #include "epilogue.hpp"
 #include "nt_gemm.hpp"
 #include "w4a16q_block.h"
@@ -165,7 +167,7 @@ __device__ __forceinline__ ScaleWay scale_way(const NtArgs& g, const Fp8Scales& 
 }
 
 // The epilogue: bias, activation, residual, eight consecutive columns of a row at a time, at any address; the last ones of a
-// row of other lengths one by one.  (1531x2050x1056 with gelu and a residual takes 18.6 us, without an epilogue 13.4: the
+// row of other lengths one by one.  (1531x2050x1056 in short sums with gelu and a residual takes 18.6 us, without an epilogue 13.4: the
 // vector units' time for gelu on the 204 compute units that have a tile.)
 struct EpiFp8 {
   struct Pre {
@@ -283,7 +285,6 @@ __global__ __launch_bounds__(C::kThreads) void fp8_kernel(const NtArgs g, const 
   // where a lane's two pieces of its row lie in 16 rows of a tile: pieces l / 16 and 4 + l / 16 (with nt_swz the 16 lanes
   // that LDS serves at a time hit distinct slots; the same in every 16 rows)
   const int ro = (own_lane & 15) * 128 + 16 * ((own_lane >> 4) ^ nt_swz(own_lane & 15));
-
   int it = 0;
   while (it < end) {
     // the lane's number, asked for anew for each tile with all that is made of it: kept over the products it spilled
@@ -597,9 +598,10 @@ __global__ __launch_bounds__(1024) void fp8_few_kernel(const FewArgs f) {
     store1(f.y, static_cast<int64_t>(row) * f.n + n0 + c, f.y_dtype, apply_epilogue(f.ep, v, row, n0 + c, f.n, f.y_dtype));
   }
 }
-// rows up to which it is taken: with codes 32 (32 rows of 4096x4096 10.2 us, on tiles 16; 64 rows of 12288x4096 40 us, on
-// tiles 17); with bf16 values 64 (64 rows of 4096x4096 16 us, on tiles 28: there all of b is first written out)
-constexpr int few_rows(int y_dtype) { return y_dtype == 0 ? 64 : 32; }
+// rows up to which it is taken, against tiles (us).  bf16 values: 64 rows of 4096x4096 16 to 28, of 12288x4096 41 to 56, of
+// 4096x12288 42 to 60: on tiles all of b is first written out.  Codes: 32 rows 10 to 13, 25 to 21, 25 to 24 (17 rows 8 to
+// 13, 18 to 21, 18 to 23; 64 rows of 12288x4096 would be 40 to 21).
+constexpr int few_rows(bool wide) { return wide ? 64 : 32; }
 
 // Both operands' codes as bf16 values: 16 codes a thread and step.  HBM bound: 3 B a code.
 struct WidenArgs {
@@ -727,13 +729,12 @@ int fp8_few(const FewArgs& f, hipStream_t s) {
 
 template <int kFa, int kFb>
 int fp8_gemm_of(const uint8_t* a, const float* sa, int64_t m, const uint8_t* b, const float* sb, bool row_b, int64_t n, int64_t k,
-                const W4Epilogue& ep, void* y, int y_dtype, void* ws, hipStream_t s) {
-  if (m <= few_rows(y_dtype)) {
+                const W4Epilogue& ep, void* y, int y_dtype, bool wide, void* ws, hipStream_t s) {
+  if (m <= few_rows(wide)) {
     const FewArgs f = {a, b, sa, sb, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), static_cast<int>(k / kBlock), ep, y, y_dtype};
-    if (y_dtype == 0) return row_b ? fp8_few<true, kFa, kFb, true>(f, s) : fp8_few<true, kFa, kFb, false>(f, s);
+    if (wide) return row_b ? fp8_few<true, kFa, kFb, true>(f, s) : fp8_few<true, kFa, kFb, false>(f, s);
     return row_b ? fp8_few<false, kFa, kFb, true>(f, s) : fp8_few<false, kFa, kFb, false>(f, s);
   }
-  const bool wide = y_dtype == 0;
   const int64_t k16 = wide ? k : k / 2;
   const NtPlan p = fp8_plan(m, n, k16);
   NtArgs g = {};
@@ -770,15 +771,17 @@ using namespace w4q;
 bool w4q_fp8_fits(int64_t m, int64_t n, int64_t k) { return nt_fits(nt_plan_tile(2, 1, m, n, k, false, 64)); }
 
 size_t w4q_fp8_gemm_workspace(int64_t m, int64_t n, int64_t k, int y_dtype) {
-  if (m <= few_rows(y_dtype)) return 0;
-  if (y_dtype != 0) return fp8_plan(m, n, k / 2).ws;
+  const bool wide = (y_dtype & W4Q_FP8_SHORT) == 0;
+  if (m <= few_rows(wide)) return 0;
+  if (!wide) return fp8_plan(m, n, k / 2).ws;
   return up256(fp8_plan(m, n, k).ws) + up256(static_cast<size_t>(2) * m * k) + up256(static_cast<size_t>(2) * n * k);
 }
 
 int w4q_launch_fp8_gemm(const uint8_t* a, int a_fmt, const float* sa, int64_t m, const uint8_t* b, int b_fmt, const float* sb,
                         int b_square, int64_t n, int64_t k, const W4Epilogue& ep, void* y, int y_dtype, void* ws, hipStream_t s) {
   auto go = [&](auto fa, auto fb) {
-    return fp8_gemm_of<decltype(fa)::value, decltype(fb)::value>(a, sa, m, b, sb, b_square == 0, n, k, ep, y, y_dtype, ws, s);
+    return fp8_gemm_of<decltype(fa)::value, decltype(fb)::value>(a, sa, m, b, sb, b_square == 0, n, k, ep, y, y_dtype & ~W4Q_FP8_SHORT,
+                                                              (y_dtype & W4Q_FP8_SHORT) == 0, ws, s);
   };
   using E4 = std::integral_constant<int, W4Q_FP8_E4M3>;
   using E5 = std::integral_constant<int, W4Q_FP8_E5M2>;
