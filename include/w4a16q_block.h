@@ -137,14 +137,14 @@ typedef struct w4q_grad {
  * grad_clip -- with that norm in fp64, out = g * c, c = fl32(1 where norm + eps <= max_norm, else
  * max_norm / (norm + eps)); a norm that is NaN makes every output NaN, an infinite one zeros (and NaN where g is
  * infinite).
- *   max_norm, eps   finite, >= 0.
+ *   max_norm, eps   finite, >= 0; taken in fp64 up to the factor's one rounding.
  *   norm       fp32 [1], device: the norm before clipping.
  *   workspace  grad_norm_workspace_size bytes, 256-B aligned (W4Q_EINVAL if smaller or NULL).
  * 1 <= n_grads <= 65536, at most 2^40 elements in all.  The tensors must not overlap one another.
  */
 int grad_norm(const w4q_grad* grads, int64_t n_grads, float* norm, void* workspace, size_t workspace_bytes,
               hipStream_t stream);
-int grad_clip(const w4q_grad* grads, int64_t n_grads, float max_norm, float eps, float* norm, void* workspace,
+int grad_clip(const w4q_grad* grads, int64_t n_grads, double max_norm, double eps, float* norm, void* workspace,
               size_t workspace_bytes, hipStream_t stream);
 int grad_norm_workspace_size(int64_t n_grads, size_t* bytes);
 

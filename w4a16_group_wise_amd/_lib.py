@@ -21,6 +21,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
 _SZ = ctypes.c_size_t
 class GemvProblem(ctypes.Structure):
     """w4q_gemv_problem of w4a16q.h"""
@@ -108,7 +109,7 @@ BLOCK_SIGNATURES = {
     "fp8_gemm": (_INT, [_P, _INT, _P, _I64, _P, _INT, _P, _INT, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _SZ, _P]),
     "fp8_gemm_workspace_size": (_INT, [_I64, _I64, _I64, _INT, _P]),
     "grad_norm": (_INT, [_P, _I64, _P, _P, _SZ, _P]),
-    "grad_clip": (_INT, [_P, _I64, _F, _F, _P, _P, _SZ, _P]),
+    "grad_clip": (_INT, [_P, _I64, _D, _D, _P, _P, _SZ, _P]),
     "grad_norm_workspace_size": (_INT, [_I64, _P]),
 }
 FP8_BLOCK = 128

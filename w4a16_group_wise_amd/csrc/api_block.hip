@@ -10,7 +10,7 @@ inline bool dtype_ok(int t) { return t == 0 || t == 1; }
 inline bool flag_ok(int t) { return t == 0 || t == 1; }
 inline uintptr_t width(int dtype) { return dtype == 0 ? 4 : 2; }
 inline bool gemm_dtype_ok(int t) { return dtype_ok(t) || t == (1 | W4Q_FP8_SHORT); }
-inline bool finite_value(float v) { return __builtin_isfinite(v); }
+inline bool finite_value(double v) { return __builtin_isfinite(v); }
 
 // scratch of exactly or more than `need` bytes (0: none is needed)
 int check_ws(const void* ws, size_t have, size_t need) {
@@ -151,9 +151,9 @@ int grad_norm_workspace_size(int64_t n_grads, size_t* bytes) {
   return W4Q_OK;
 }
 
-static int grads_call(const w4q_grad* grads, int64_t n_grads, bool clip, float max_norm, float eps, float* norm, void* workspace,
+static int grads_call(const w4q_grad* grads, int64_t n_grads, bool clip, double max_norm, double eps, float* norm, void* workspace,
                       size_t workspace_bytes, hipStream_t stream) {
-  if (!norm || !finite_value(max_norm) || max_norm < 0.0f || !finite_value(eps) || eps < 0.0f) return W4Q_EINVAL;
+  if (!norm || !finite_value(max_norm) || max_norm < 0.0 || !finite_value(eps) || eps < 0.0) return W4Q_EINVAL;
   int rc = check_grads(grads, n_grads, clip);
   if (rc != W4Q_OK) return rc;
   if (!aligned(norm, 4)) return W4Q_EALIGN;
@@ -163,10 +163,10 @@ static int grads_call(const w4q_grad* grads, int64_t n_grads, bool clip, float m
 
 int grad_norm(const w4q_grad* grads, int64_t n_grads, float* norm, void* workspace, size_t workspace_bytes,
               hipStream_t stream) {
-  return grads_call(grads, n_grads, false, 0.0f, 0.0f, norm, workspace, workspace_bytes, stream);
+  return grads_call(grads, n_grads, false, 0.0, 0.0, norm, workspace, workspace_bytes, stream);
 }
 
-int grad_clip(const w4q_grad* grads, int64_t n_grads, float max_norm, float eps, float* norm, void* workspace,
+int grad_clip(const w4q_grad* grads, int64_t n_grads, double max_norm, double eps, float* norm, void* workspace,
               size_t workspace_bytes, hipStream_t stream) {
   return grads_call(grads, n_grads, true, max_norm, eps, norm, workspace, workspace_bytes, stream);
 }

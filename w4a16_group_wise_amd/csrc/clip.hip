@@ -114,12 +114,12 @@ __global__ __launch_bounds__(256) void clip_norm_kernel(const double* __restrict
   if (threadIdx.x == 0) *norm = static_cast<float>(__builtin_sqrt(s));
 }
 
-__global__ __launch_bounds__(256) void clip_scale_kernel(const ClipTable t, const double* __restrict__ parts, float max_norm,
-                                                         float eps, float* __restrict__ norm_out) {
+__global__ __launch_bounds__(256) void clip_scale_kernel(const ClipTable t, const double* __restrict__ parts, double max_norm,
+                                                         double eps, float* __restrict__ norm_out) {
   const double norm = __builtin_sqrt(sum_parts(parts, t.sums));
   if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
-  const double top = norm + static_cast<double>(eps);
-  const float c = top <= static_cast<double>(max_norm) ? 1.0f : static_cast<float>(static_cast<double>(max_norm) / top);
+  const double top = norm + eps;
+  const float c = top <= max_norm ? 1.0f : static_cast<float>(max_norm / top);
   if (c == 1.0f && t.in_place != 0) return;
   clip_pieces(t, [&](const void* g, int g_dtype, void* out, int out_dtype, int64_t begin, int n) {
     if (c == 1.0f && out == g) return;
@@ -148,7 +148,7 @@ using namespace w4q;
 
 size_t w4q_clip_workspace(int64_t) { return kMostBlocks * sizeof(double); }
 
-int w4q_launch_clip(const w4q_grad* grads, int64_t n_grads, bool scale, float max_norm, float eps, float* norm, void* ws,
+int w4q_launch_clip(const w4q_grad* grads, int64_t n_grads, bool scale, double max_norm, double eps, float* norm, void* ws,
                     hipStream_t s) {
   double* parts = static_cast<double*>(ws);
   int sums = 0;

@@ -268,7 +268,7 @@ int w4q_launch_fp8_gemm(const uint8_t* a, int a_fmt, const float* sa, int64_t m,
                         int b_square, int64_t n, int64_t k, const w4q::W4Epilogue& ep, void* y, int y_dtype, void* ws,
                         hipStream_t s);
 size_t w4q_clip_workspace(int64_t n_grads);
-int w4q_launch_clip(const w4q_grad* grads, int64_t n_grads, bool scale, float max_norm, float eps, float* norm, void* ws,
+int w4q_launch_clip(const w4q_grad* grads, int64_t n_grads, bool scale, double max_norm, double eps, float* norm, void* ws,
                     hipStream_t s);
 
 static inline int w4q_launch_status() {
