@@ -39,7 +39,7 @@ typedef struct w4q_norm_params {
  *   n = r / rms(r) * (w_pre + weight_offset)             (of the unrounded r)
  *   h       [m][d] fp32 or bf16 (h_dtype).
  *   y       [m][d] (y_dtype) or NULL: no block's output; then n is h's norm, w_pre and n are needed, w_post,
- *           gate and r must be NULL and the scales are not used.
+ *           gate and r must be NULL and the scales are not used (here and in the backward call).
  *   w_post, w_pre   fp32 [d] or NULL; w_pre and n are given together, or neither (r alone).
  *   gate    [gate_rows][d] (gate_dtype) or NULL; m a multiple of gate_rows, row i of m takes gate row
  *           i / (m / gate_rows): one gate for all rows (gate_rows 1), one for each sequence, or one for each row.
@@ -63,7 +63,8 @@ int block_norm_fwd(const void* h, int h_dtype, const void* y, int y_dtype, int64
  *   grad_r  [m][d] of r's type or NULL: what reaches r from further on.  Not both NULL.
  *   r       [m][d] (r_dtype); may be NULL without grad_n.  (Without y: r is h.)
  *   y       [m][d] (y_dtype) or NULL as in the forward; may also be NULL where neither w_post nor a gate's
- *           gradient needs it; with y or grad_y the branch exists.
+ *           gradient needs it; with y, grad_y or a gate the branch exists.  Without all three the forward had no y:
+ *           the scales are not used there, and not here (grad_h = dr).
  *   grad_h  [m][d] of r's type, or NULL; may be grad_r itself.  grad_y [m][d] (y_dtype) or NULL.
  *   grad_w_post, grad_w_pre   fp32 [d] or NULL.  grad_gate [gate_rows][d] of the gate's type or NULL.
  *           At least one output.  Each needs its inputs: grad_w_pre grad_n, grad_w_post w_post, grad_gate gate.

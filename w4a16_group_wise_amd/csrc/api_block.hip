@@ -103,8 +103,10 @@ int block_norm_bwd(const void* grad_n, int n_dtype, const void* grad_r, const vo
       !aligned(grad_w_post, 4) || !aligned(grad_w_pre, 4) || !aligned(grad_gate, gw))
     return W4Q_EALIGN;
   if ((rc = check_ws(workspace, workspace_bytes, w4q_norm_bwd_workspace(m, d))) != W4Q_OK) return rc;
+  w4q_norm_params p = *hp;
+  if (!y && !grad_y && !gate) p.skip_scale = 1.0f;  // no branch: the forward used h as it was
   return w4q_launch_norm_bwd(grad_n, n_dtype, grad_r, r, r_dtype, y, y_dtype, m, d, w_post, w_pre, gate, gate_dtype, gate_rows,
-                             *hp, grad_h, grad_y, grad_w_post, grad_w_pre, grad_gate, workspace, stream);
+                             p, grad_h, grad_y, grad_w_post, grad_w_pre, grad_gate, workspace, stream);
 }
 
 int fp8_quant(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt, int square, uint8_t* codes, float* scale,

@@ -697,7 +697,8 @@ def block_norm_bwd(grad_n: Optional[torch.Tensor], grad_r: Optional[torch.Tensor
     """Gradients of block_norm_fwd from its r (as stored; h where there was no y) and y, grad_n (None without w_pre) and
     grad_r, what reaches r from further on (or None).  -> (grad_h [m][d] of r's type, grad_y of y's type | None,
     grad_w_post fp32 [d] | None, grad_w_pre fp32 [d] | None, grad_gate of the gate's shape and type | None), each
-    where its tensor is given (y, which only w_post and a gate need, also brings grad_y); with_h False leaves grad_h out,
+    where its tensor is given (y, which only w_post and a gate need, also brings grad_y; without y, as in the forward, there
+    is no skip_scale); with_h False leaves grad_h out,
     inplace puts it into grad_r."""
     first = next((t for t in (grad_n, grad_r) if t is not None), None)
     if first is None:
@@ -720,6 +721,8 @@ def block_norm_bwd(grad_n: Optional[torch.Tensor], grad_r: Optional[torch.Tensor
     gdt, grows = _norm_inputs(m, d, dev, w_post, w_pre, gate)
     if y is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate need y")
+    if y is None and skip_scale != 1.0:
+        raise ValueError("skip_scale needs y")
     if inplace and (grad_r is None or not with_h):
         raise ValueError("inplace needs grad_r and with_h")
     if inplace:
