@@ -7,6 +7,7 @@ from __future__ import annotations
 
 from typing import Optional, Tuple
 
+import bisect
 import ctypes
 import functools
 import torch
@@ -845,6 +846,7 @@ class GradPlan:
             if begin < end:
                 raise ValueError(f"{n} and {other} overlap")
         self._keep = (grads, outs)
+        self._begins, self._spans = [s[0] for s in spans], spans
         self._arr = arr
         self._ptr = ctypes.cast(arr, ctypes.c_void_p)
         self._n = len(grads)
@@ -854,6 +856,11 @@ class GradPlan:
     def _run(self, fn: str, out, *args) -> torch.Tensor:
         with _OnDevice(self.device):
             norm = _out(out, "out", (1,), torch.float32, self.device)
+            if out is not None:   # the spans are apart and in order: the last that begins before out's end decides
+                begin = norm.data_ptr()
+                i = bisect.bisect_left(self._begins, begin + 4) - 1
+                if i >= 0 and self._spans[i][1] > begin:
+                    raise ValueError(f"out and {self._spans[i][2]} overlap")
             # (a workspace a call: calls on several streams and captured graphs share nothing)
             ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
             check(fn, getattr(lib(), fn)(self._ptr, self._n, *args, norm.data_ptr(), ws.data_ptr(), self._bytes,
