@@ -282,15 +282,15 @@ __global__ __launch_bounds__(C::kThreads) void fp8_kernel(const NtArgs g, const 
   int vo[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) vo[q] = OpA::load_off(q, own_lane, g.lda);
-  // where a lane's two pieces of its row lie in 16 rows of a tile: pieces l / 16 and 4 + l / 16 (with nt_swz the 16 lanes
-  // that LDS serves at a time hit distinct slots; the same in every 16 rows)
-  const int ro = (own_lane & 15) * 128 + 16 * ((own_lane >> 4) ^ nt_swz(own_lane & 15));
   int it = 0;
   while (it < end) {
     // the lane's number, asked for anew for each tile with all that is made of it: kept over the products it spilled
     int zero = 0;
     asm volatile("" : "+s"(zero));
     const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+    // where a lane's two pieces of its row lie in 16 rows of a tile: pieces l / 16 and 4 + l / 16 (with nt_swz the 16 lanes
+    // that LDS serves at a time hit distinct slots; the same in every 16 rows)
+    const int ro = (lane & 15) * 128 + 16 * ((lane >> 4) ^ nt_swz(lane & 15));
     int t, s0, s1;
     if (it < whole_end) {
       t = it / g.S * g.nblk + lb;
