@@ -82,8 +82,11 @@ __device__ __forceinline__ void block_sum(float (&v)[N], int waves, SumBuf* buf)
 // eight columns and skips those that are the thread's before it: they count as zeros and are not stored.  kShort: rows of
 // fewer than eight columns, one by one, on thread 0.  Rows need no alignment (one element at a time 1531x1001 took 47 us
 // backwards, not 15).
+// kAnew: comparisons with skip, d and a type are made anew for each row.  Their masks, kept over the rows, take more scalar
+// registers than there are (up to 66 spilled, to lanes of a vector register), but in the forward kernel of one chunk, where
+// making them anew costs (1531x1001 7.3 -> 7.9 us).
 enum Kind { kWhole, kTail, kShort };
-template <Kind K>
+template <Kind K, bool kAnew = true>
 struct Cols {
   int first, skip, d;
   bool some;
@@ -101,19 +104,31 @@ struct Cols {
     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
     if (p == nullptr || !some) return;
     const int64_t o = row * d + first;
+    if (kAnew && !__builtin_constant_p(dtype)) asm volatile("" : "+s"(dtype));
     if constexpr (K == kShort) {
+      const int n = skipped();
 #pragma unroll
       for (int e = 0; e < 7; ++e)
-        if (e < d) v[e] = dtype == 0 ? static_cast<const float*>(p)[o + e] : bf16_val(static_cast<const uint16_t*>(p)[o + e]);
+        if (e < n) v[e] = dtype == 0 ? static_cast<const float*>(p)[o + e] : bf16_val(static_cast<const uint16_t*>(p)[o + e]);
     } else {
       u32x4 a, b;
       load8_any(p, o, dtype, a, b);
       unpack8(a, b, dtype, v);
       if constexpr (K == kTail) {
+        const int n = skipped();
 #pragma unroll
-        for (int e = 0; e < 7; ++e) v[e] = e < skip ? 0.0f : v[e];
+        for (int e = 0; e < 7; ++e) v[e] = e < n ? 0.0f : v[e];
       }
     }
+  }
+  // what a group of comparisons is with: skip, or for short rows d
+  __device__ __forceinline__ int skipped() const {
+    int n = K == kShort ? d : skip;
+    if constexpr (kAnew && K == kShort)
+      asm volatile("" : "+s"(n));
+    else if constexpr (kAnew)
+      asm volatile("" : "+v"(n));
+    return n;
   }
   // a weight: plus the offset; ones without one
   __device__ __forceinline__ void weight(const float* w, float offset, float (&v)[8]) const {
@@ -124,10 +139,12 @@ struct Cols {
   __device__ __forceinline__ void store(void* p, int64_t row, int dtype, const float (&v)[8]) const {
     if (!some) return;
     const int64_t o = row * d + first;
+    if (kAnew && !__builtin_constant_p(dtype)) asm volatile("" : "+s"(dtype));
     if (K == kShort || (K == kTail && skip != 0)) {
+      const int n = skipped();
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (K == kShort ? e < d : e >= skip) store1(p, o + e, dtype, v[e]);
+        if (K == kShort ? e < n : e >= n) store1(p, o + e, dtype, v[e]);
     } else {
       store8_any(p, o, dtype, v);
     }
@@ -149,13 +166,14 @@ struct NormArgs {
 
 template <Kind K, int C>
 __global__ __launch_bounds__(K == kShort ? 64 : 1024) void norm_fwd_kernel(const NormArgs a) {
+  using At = Cols<K, C == 2>;
   __shared__ SumBuf red[2][1];
   const int waves = blockDim.x >> 6;
   clear_sums(red[0], 2);
   float wpost[C][8], wpre[C][8], gate[C][8];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const Cols<K> at(c, a.d);
+    const At at(c, a.d);
     at.weight(a.w_post, a.hp.weight_offset, wpost[c]);
     at.weight(a.w_pre, a.hp.weight_offset, wpre[c]);
     at.load(a.gate, 0, a.gate_dtype, gate[c]);
@@ -168,7 +186,7 @@ __global__ __launch_bounds__(K == kShort ? 64 : 1024) void norm_fwd_kernel(const
     float s[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const Cols<K> at(c, a.d);
+      const At at(c, a.d);
       at.load(a.y, row, a.y_dtype, y[c]);
       at.load(a.h, row, a.h_dtype, r[c]);
       if (a.gate_rows > 1) at.load(a.gate, row / a.run, a.gate_dtype, gate[c]);
@@ -192,7 +210,7 @@ __global__ __launch_bounds__(K == kShort ? 64 : 1024) void norm_fwd_kernel(const
           if (a.gate != nullptr) u *= gate[c][e];
           r[c][e] = __builtin_fmaf(a.hp.branch_scale, u, a.hp.skip_scale * r[c][e]);
         }
-        if (a.r != nullptr) Cols<K>(c, a.d).store(a.r, row, a.h_dtype, r[c]);
+        if (a.r != nullptr) At(c, a.d).store(a.r, row, a.h_dtype, r[c]);
       }
     }
     if (a.n == nullptr) continue;
@@ -208,7 +226,7 @@ __global__ __launch_bounds__(K == kShort ? 64 : 1024) void norm_fwd_kernel(const
     for (int c = 0; c < C; ++c) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) r[c][e] = r[c][e] * b * wpre[c][e];
-      Cols<K>(c, a.d).store(a.n, row, a.n_dtype, r[c]);
+      At(c, a.d).store(a.n, row, a.n_dtype, r[c]);
     }
   }
 }
@@ -476,7 +494,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_ahead_kernel(const NormBwdArgs 
   for (int i = row0; i < row1; ++i) {
     const int row = __builtin_amdgcn_readfirstlane(i);
     Row x = ahead;
-    if (K == kTail && at.skip != 0) x.gn.clear(at.skip), x.r.clear(at.skip), x.y.clear(at.skip), x.gr.clear(at.skip);
+    if (K == kTail && at.skip != 0) {
+      const int n = at.skipped();
+      x.gn.clear(n), x.r.clear(n), x.y.clear(n), x.gr.clear(n);
+    }
     if (row + 1 < row1) load(row + 1, ahead);
     if (row / a.run != g) {
       flush_gate(g);
