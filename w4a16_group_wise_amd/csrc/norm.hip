@@ -258,11 +258,6 @@ __device__ __forceinline__ f32x4 row_factors(const NormBwdArgs& a, const float (
   return f;
 }
 
-// y where it has a norm, and 0 otherwise: then an infinity there is not to reach dy (0 times it is no number)
-__device__ __forceinline__ float normed(const NormBwdArgs& a, float y) {
-  return __builtin_bit_cast(float, __builtin_bit_cast(int, y) & (a.w_post != nullptr ? -1 : 0));
-}
-
 // kMode 0: everything, for rows of up to 8192 columns.  Longer rows take two launches: kMode 1 takes a row's sums and
 // leaves its four factors, kMode 2 makes the gradients of 8192 columns (blockIdx.y) from them.
 template <Kind K, int kMode>
@@ -369,6 +364,7 @@ __global__ __launch_bounds__(K == kShort ? 64 : 1024) void norm_bwd_kernel(const
         s_post[e] = __builtin_fmaf(du, yb, s_post[e]);
         s_gate[e] = __builtin_fmaf(a.hp.branch_scale * dr, yb * v.wpost[e], s_gate[e]);
         dh[e] = a.hp.skip_scale * dr;
+        // (without a norm an infinity in y is not to reach dy: 0 times it is no number)
         dy[e] = f[2] * (du * v.wpost[e] - (a.w_post != nullptr ? f[3] * yb : 0.0f));
       }
       if (a.gh != nullptr) at.store(a.gh, row, a.r_dtype, dh);
