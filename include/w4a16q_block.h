@@ -93,8 +93,8 @@ enum w4q_fp8_format { W4Q_FP8_E4M3 = 0 /* largest 448, no infinities */, W4Q_FP8
  *   scale   fp32 [rows][kp / 128], or with square [ceil(rows / 128)][kp / 128]; with codes.
  *   codes_t, scale_t   the same of the transpose of x ([cols][rp], rp = rows rounded up; its own blocks run along
  *           the rows of x), or NULL.  At least one of the two forms; both take one pass over x.
- * A block of zeros has scale 0; one with a NaN or an infinity has scale NaN (and codes 0), so that what is made of
- * it is NaN.
+ * A block of zeros, or of values whose largest gives a quotient that rounds to zero (at most 2^-150), has scale 0 and
+ * codes 0; one with a NaN or an infinity has scale NaN (and codes 0), so that what is made of it is NaN.
  *   x [rows][cols] fp32 or bf16, element-aligned; codes 16-B aligned.  rows, cols <= 2^22 (else W4Q_EUNSUPPORTED).
  */
 int fp8_quant(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt, int square, uint8_t* codes, float* scale,
@@ -112,7 +112,8 @@ int fp8_quant(const void* x, int x_dtype, int64_t rows, int64_t cols, int fmt, i
  *   y_dtype  0 fp32, 1 bf16, or 1 | W4Q_FP8_SHORT: bf16 from the 8-bit matrix cores' own sums, at up to twice the rate.
  * Every product is exact and every sum fp32's.  With W4Q_FP8_SHORT the matrix cores cut each of 8 consecutive k's products
  * off below 2^-13 of the largest of them (7 2^-13 of that at most in all); the sums of eights, and of the blocks, are
- * fp32's there too.  a_scale * b_scale is rounded to fp32: below 2^-126 it keeps fewer digits.
+ * fp32's there too.  a_scale * b_scale is rounded to fp32 and must stay in its range: below 2^-126 it keeps fewer digits,
+ * and from 2^128 on it is infinite: so is what the block adds then, or no number where its sum of codes is zero.
  *   workspace  fp8_gemm_workspace_size bytes, 256-B aligned (W4Q_EINVAL if smaller, or NULL where it is not 0).
  *   Limits: m, n < 2^30, k <= 2^22, at most 2^30 halves of blocks of k over all 64 x 64 output tiles and at most
  *   2^24 - 16 of the tiles (W4Q_EUNSUPPORTED).

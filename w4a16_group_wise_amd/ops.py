@@ -788,9 +788,9 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
              short_sums: bool = False, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [m][n] = act(A B^T + bias) + residual for A [m][k] and B [n][k] as fp8_quant holds them: codes float8_e4m3fn or
     float8_e5m2 with k a multiple of 128, a_scale fp32 [m][k / 128], b_scale fp32 [n][k / 128] or (square blocks)
-    [ceil(n / 128)][k / 128].  bias fp32 [n]; residual of y's type (may be `out` itself).  All sums are fp32's; with
-    short_sums (bf16 results only) those of 8 consecutive k are the 8-bit matrix cores', which cut products off below 2^-13
-    of the largest of the eight, at up to twice the rate."""
+    [ceil(n / 128)][k / 128], the two scales' products inside fp32's range.  bias fp32 [n]; residual of y's type (may be
+    `out` itself).  All sums are fp32's; with short_sums (bf16 results only) those of 8 consecutive k are the 8-bit matrix
+    cores', which cut products off below 2^-13 of the largest of the eight, at up to twice the rate."""
     af, m, k = _codes(a, "a")
     bf, n, kb = _codes(b, "b", a.device)
     if kb != k:
@@ -883,7 +883,8 @@ def grad_norm(grads) -> torch.Tensor:
 
 def grad_clip(grads, max_norm: float, *, eps: float = 1e-6, outs=None) -> torch.Tensor:
     """grads scaled by min(1, max_norm / (norm + eps)), in place or into outs; -> the norm before, fp32 [1] on the device.
-    For gradients that stay in their buffers, GradPlan marshals the list once."""
+    For gradients that stay in their buffers, GradPlan marshals the list once: checking and marshalling takes 1.8 us a
+    tensor (300 of them 0.57 ms a call, with a plan 0.03), as long as the kernels take for 0.8 M elements."""
     return GradPlan(grads, outs).clip(max_norm, eps=eps)
 
 
