@@ -18,8 +18,9 @@
 // A gate row's sum that lies in one workgroup's rows is stored right away; where it spans several, each leaves
 // its piece.
 //
-// HBM bound: every tensor is read or written once (backwards, past 8192 columns, read twice).  8192x4096, residual stream in fp32, y and n in bf16: forwards 70 us
-// (5.7 TB/s), backwards 124 and 7 for the sums over workgroups (4.8 TB/s); one row of 4096 forwards 2.6.
+// HBM bound: every tensor is read or written once (backwards, past 8192 columns, read twice).  8192x4096, residual stream in
+// fp32, y and n in bf16: forwards 75 us (5.4 TB/s), backwards 127 and 7 for the sums over workgroups (4.5 TB/s); one row of
+// 4096 forwards 3.2; 2048x12288 bf16 forwards 41, backwards 136.
 #include "epilogue.hpp"
 #include "w4a16q_block.h"
 
