@@ -123,3 +123,9 @@ def test_past_32_bits(dev, m, n, k):
         for t in (slice(0, 11), slice(n - 13, n)):
             ref, err = B.gemm(a[s], sa[s], b[t], sb[t], short=True)
             within(y[s, t], ref, err, "y")
+
+
+def test_short_sums_are_refused_for_fp32_results(dev):
+    a, sa, b, sb = operands(dev, 8, 64, 256, "e4m3", "e4m3", True)
+    with pytest.raises(ValueError, match="bf16"):
+        w4q.fp8_gemm(a, sa, b, sb, out_dtype=torch.float32, short_sums=True)

@@ -652,7 +652,9 @@ constexpr Fp8Tile kFp8Tiles[3] = {{256, 1, 1.75, 1.55, 5.0}, {128, 2, 0.62, 0.70
 // The cheapest of: one tile of each size per workgroup, and whole tiles with the remaining ones' stages in ranges,
 // whose partial tiles then pass through memory once more.  k16: 16-bit values of a row (half the codes, or the
 // bf16 values).  Measured whole: 64 rows of 4096x4096 codes 16 us on tiles of 64, 26 on 128, 52 on 256; 1024 rows 38, 28,
-// 57; 2048 rows 62, 46, 58; 4096 rows 122, 86, 66.
+// 57; 2048 rows 62, 46, 58; 4096 rows 122, 86, 66.  As bf16 values, with their copies: 200 rows 38, 61, 115; 1024 rows 76, 65,
+// 118; 2048 rows of 12288x4096 370, 277, 250.  Over 65 to 2048 rows of 4096x4096, 2050x1152 and 12288x4096 no other tile or
+// split took less than 0.91 of the chosen one's time.
 NtPlan fp8_plan(int64_t M, int64_t N, int64_t k16) {
   NtPlan best = {};
   double best_us = 0.0;
