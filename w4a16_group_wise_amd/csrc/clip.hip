@@ -13,7 +13,8 @@
 // own for each the scaling of 386 M fp32 gradients took 660 us, not 620.  (One workgroup for each piece and the sums
 // joined by a launch between: 600, but 10 to 70 more where nothing is to be scaled.)
 //
-// HBM bound: two reads and a write of every gradient.  386 M elements, fp32 to fp32: 882 us (the profile's kernels 294 and 602), 5.2 TB/s.
+// HBM bound: two reads and a write of every gradient.  386 M elements, fp32 to fp32: 882 us (under the profiler 294 for the
+// norm and 602), 5.2 TB/s.
 #include "epilogue.hpp"
 #include "w4a16q_block.h"
 

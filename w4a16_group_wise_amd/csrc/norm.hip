@@ -83,9 +83,9 @@ __device__ __forceinline__ void block_sum(float (&v)[N], int waves, SumBuf* buf)
 // eight columns and skips those that are the thread's before it: they count as zeros and are not stored.  kShort: rows of
 // fewer than eight columns, one by one, on thread 0.  Rows need no alignment (one element at a time 1531x1001 took 47 us
 // backwards, not 15).
-// kAnew: comparisons with skip, d and a type are made anew for each row.  Their masks, kept over the rows, take more scalar
-// registers than there are (up to 66 spilled, to lanes of a vector register), but in the forward kernel of one chunk, where
-// making them anew costs (1531x1001 7.3 -> 7.9 us).
+// kAnew: comparisons with skip, d and a type are made anew for each row, as their masks, kept over the rows, take more scalar
+// registers than there are (up to 66 spilled, to lanes of a vector register).  Off in the forward kernel of one chunk, which
+// has registers for them (1531x1001 7.3 us, made anew 7.9).
 enum Kind { kWhole, kTail, kShort };
 template <Kind K, bool kAnew = true>
 struct Cols {
