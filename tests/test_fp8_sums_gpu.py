@@ -32,7 +32,7 @@ def test_bf16_results_have_the_sums_of_fp32(dev, m):
 def cut_off(a, sa, b, sb):
     """What short sums may lose, in 64 bits.  A code has 4 bits, so a product 8: its last place is 2^-8 of it or more.  Of an eight's
     products those of 2^-5 of the largest and more reach no lower than 2^-13 of it and lose nothing; one below loses less than
-    2^-13 of the largest, and never more than itself."""
+    2^-13 of the largest, and never more than itself.  (On normal values about a ninth of 7 2^-13 of all magnitudes.)"""
     k = a.shape[1]
     p = (a.float()[:, None, :] * b.float()[None, :, :]).double().abs()      # exact: 8 bits
     p = p.view(*p.shape[:2], -1, 8)
